@@ -66,7 +66,10 @@ typedef enum {
   DSA_ERR_RANGE = 8         /* an input value lies outside the range a kernel supports   */
 } dsa_status;
 
-typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1 } dsa_dtype;
+/* DSA_F16 and DSA_F32 are element types of dsa_rope and of the rows that dsa_latent_append takes; DSA_MXFP4 is a
+ * row format of paged latent caches (below). */
+typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_MXFP4 = 2, DSA_F16 = 3, DSA_F32 = 4 } dsa_dtype;
+#define DSA_MXFP4_ROW 320 /* bytes of a 4-bit latent row */
 
 /*
  * A token-major cache (indexer keys: dim 128; latent KV: dim 576), dense or paged.
@@ -76,7 +79,14 @@ typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1 } dsa_dtype;
  *          scale [n_pages, 64]; sequence b's token s lives in physical page
  *          block_table[b * max_pages + s / 64], slot s % 64; seq_lens[b] = tokens of b.
  *          n_tokens = n_pages * 64 (used for bounds checks of page ids).
- * bf16 caches have scale == NULL.  Paged caches are e4m3 only.
+ * bf16 caches have scale == NULL.  Paged caches are e4m3 or, for latent rows (dim 576), MXFP4.
+ *   MXFP4  (paged, dim 576): data [n_pages, 64, 320] bytes, row_stride = DSA_MXFP4_ROW, scale == NULL,
+ *          n_tokens < 2^31.  A row holds 18 blocks of 32 values; a value is c * 2^e with c one of
+ *          +-{0, .5, 1, 1.5, 2, 3, 4, 6} (e2m1, 4 bits) and e its block's exponent, -13 <= e <= 13.
+ *          Bytes 0..287: 72 little-endian 32-bit words of 8 values; bits 4i..4i+2 of a word are the
+ *          magnitude code of value i, bit 8i + 7 is the sign of value i for i < 4, bit 8i + 3 the sign
+ *          of value 4 + i.  Bytes 288..305: e + 127 of blocks 0..17 (255: every value of the block is
+ *          NaN; other bytes outside 114..140 are read as the nearer end).  Bytes 306..319 are zero.
  */
 typedef struct {
   const void* data;
@@ -195,7 +205,8 @@ dsa_status dsa_topk(const float* scores, int64_t ld, int32_t n_rows, const int32
  *   idx  [n_q / q_rows_per_idx_row, k] int32; query row r uses idx row r / q_rows_per_idx_row
  *        (MTP rows sharing row 0's selection).  -1 entries are skipped.
  *   kv   dim 576.  Dense bf16: idx values are token rows of kv.  Paged e4m3: idx row i is
- *        sequence i and its values are token positions s < seq_lens[i].
+ *        sequence i and its values are token positions s < seq_lens[i].  Paged MXFP4: the same;
+ *        q may hold any finite bf16 value, and a head whose q is not finite gets NaN.
  *   A row with no valid index gets out = 0 and lse = -inf.
  *   Paged e4m3 caches: the products run on f16 operands (e4m3 values are exact in f16), so q is
  *   converted from bf16 to f16 and must lie within the f16 range, |q| < 65520; a larger value
@@ -223,7 +234,8 @@ dsa_status dsa_sparse_mla_attn(const void* q, const dsa_cache_view* kv, const in
  *                  dense keys are quantised too)
  *   q_pos0: position of prefill query row 0 (ignored for paged caches)
  *   q_rows_per_idx_row: 1 in prefill, 1 + d in decode with d MTP draft rows
- *   q[l] [n_idx_rows * q_rows_per_idx_row, 64, 576] bf16, kv[l] dim 576, out[l], lse[l]
+ *   q[l] [n_idx_rows * q_rows_per_idx_row, 64, 576] bf16, kv[l] dim 576 (dense bf16, paged e4m3 or paged
+ *   MXFP4, each layer its own), out[l], lse[l]
  *   workspace: at least dsa_group_workspace_bytes(a) bytes of device memory: e4m3 copies of
  *              the indexer inputs (when quantised here), the scores of one chunk of query rows
  *              (rows x causal length <= max(64 MB, 2,048 x longest row x 4 B), at most 1 GB),
@@ -325,6 +337,73 @@ dsa_status dsa_mla_latent(const void* x, const void* Wkv, const float* gamma, co
 dsa_status dsa_rope_query(void* q, const int32_t* pos, int32_t n_q, float theta, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Rotary positions in general (dsa_rope_query is the fixed form for this path's queries): the rotated dims of
+ * every head, in one of two layouts, with the angle rules for contexts longer than the trained one.
+ *
+ * dsa_rope_plan_init fills a plan on the host (no device work): pair i of the rot_dim rotated dims turns by
+ * pos * inv_freq[i], both in double.  With f_i = theta^(-2i / rot_dim):
+ *   DSA_ROPE_PLAIN   inv_freq[i] = f_i
+ *   DSA_ROPE_LINEAR  inv_freq[i] = f_i / factor (position interpolation)
+ *   DSA_ROPE_NTK     f_i with theta * factor^(rot_dim / (rot_dim - 2)) in theta's place
+ *   DSA_ROPE_YARN    inv_freq[i] = f_i (1 - g_i) + f_i / factor * g_i, g_i = clamp((i - low) / (high - low), 0, 1),
+ *                    low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)), rot_dim - 1),
+ *                    d(n) = rot_dim ln(original_len / (2 pi n)) / (2 ln theta)
+ * The rotated values are multiplied by mscale (<= 0: the rule's own, 0.1 ln(factor) + 1 for YaRN, else 1).
+ * Layouts: DSA_ROPE_INTERLEAVED pairs dims (2i, 2i + 1), DSA_ROPE_HALF dims (i, i + rot_dim / 2).
+ *   rot_dim: a multiple of 16, at most 256.  theta > 1, factor >= 1; YaRN: original_len > 0,
+ *   beta_fast >= beta_slow > 0; NTK: rot_dim > 2.  factor, original_len and the betas are ignored where unused.
+ *
+ * dsa_rope: dims [offset, offset + rot_dim) of every head of x [n_tokens, n_heads, dim] turned to pos[token]
+ * (int32 [n_tokens] on the device, of either sign), each value rounded once to dtype (bf16, f16 or f32):
+ *   out[a] = mscale (x[a] cos - x[b] sin),  out[b] = mscale (x[a] sin + x[b] cos)  for each pair (a, b).
+ * out == x with equal strides works in place and touches the rotated dims only; otherwise out must not overlap x
+ * and receives the other dims unchanged.  backward != 0 applies the transposed map (the angle negated, mscale
+ * kept): the gradient of x from the gradient of out.
+ *   Strides are in elements; strides and offset are multiples of 16 bytes, pointers 16-byte aligned, and so are
+ *   dim and offset + rot_dim; out's heads and tokens must not overlap.
+ */
+#define DSA_ROPE_MAX_PAIRS 128
+enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };
+typedef struct {
+  double inv_freq[DSA_ROPE_MAX_PAIRS];
+  double mscale;
+  int32_t rot_dim;
+  int32_t layout;
+} dsa_rope_plan;
+dsa_status dsa_rope_plan_init(dsa_rope_plan* plan, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                              double factor, double original_len, double beta_fast, double beta_slow, double mscale);
+dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t dtype, const int32_t* pos,
+                    int32_t n_tokens, int32_t n_heads, int32_t dim, int32_t offset, int64_t x_token_stride,
+                    int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride, int32_t backward,
+                    void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * New latent rows into a paged cache, normalised, rotated and quantised on the way in one launch:
+ *   y[r] = [ x[r, :512] / sqrt(mean(x[r, :512]^2) + eps) * gamma  ||  rope(x[r, 512:], pos[r]) ]
+ * (gamma NULL: the first 512 dims as they are; rope NULL: the last 64 as they are), formed in double, rounded to
+ * fp32, and stored at position pos[r] of sequence seq[r] (r itself when seq is NULL) of `cache`:
+ *   e4m3    the rule of dsa_cache_write_e4m3 (one scale per row);
+ *   MXFP4   per block of 32: e = the least exponent of [-13, 13] with amax <= 6 * 2^e, c = RNE(y / 2^e), magnitudes
+ *           above 6 * 2^13 saturating; a block with a NaN reads back as NaN.
+ *   x         [n_rows, 576] bf16 or f32, row stride x_stride elements (a multiple of 16 bytes)
+ *   rope      a plan with rot_dim 64, or NULL
+ *   cache     paged, dim 576, e4m3 or MXFP4: its pages and scales are written, its seq_lens not read (may be NULL)
+ * Each (sequence, position) may appear at most once per call.  A row whose sequence, position or page is out of
+ * range is skipped and reported as DSA_ERR_BOUNDS by dsa_sync_status.
+ *
+ * dsa_latent_read: rows back out of a paged cache as bf16, out[r] = the values at position pos[r] of sequence
+ * seq[r] (4-bit values are exact in bf16; an e4m3 code times its scale is rounded once).  A row that is out of
+ * range, or at or past seq_lens, is left as it was and reported in the same way.  out [n_rows, 576] with row
+ * stride out_stride elements (a multiple of 8).
+ */
+dsa_status dsa_latent_append(const void* x, int32_t x_dtype, int64_t x_stride, int32_t n_rows, const float* gamma,
+                             double eps, const dsa_rope_plan* rope, const int32_t* seq, const int32_t* pos,
+                             const dsa_cache_view* cache, void* stream);
+dsa_status dsa_latent_read(const dsa_cache_view* cache, const int32_t* seq, const int32_t* pos, int32_t n_rows,
+                           void* out_bf16, int64_t out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Split-N decode of one long sequence over G GPUs (the pages' full 1M context starts at 8 B200s
  * with an FP8 KV cache, ailearn deployment section "CP · EP · P/D · HiCache"; the split itself is
  * this library's design).  Rank r holds the contiguous cache slice of positions [lo_r, hi_r) and
@@ -366,7 +445,7 @@ const char* dsa_status_str(dsa_status s);
 const char* dsa_last_error(void);       /* thread-local text of the last failure; never NULL */
 int32_t dsa_abi_version(void);
 /* sizeof of the ABI structs as compiled into the library (0: dsa_cache_view,
- * 1: dsa_index_handle, 2: dsa_group_args), so bindings can check their own layout. */
+ * 1: dsa_index_handle, 2: dsa_group_args, 3: dsa_rope_plan), so bindings can check their own layout. */
 size_t dsa_abi_sizeof(int32_t which);
 /* Synchronise the stream, then read and clear the device status word of the current
  * device: DSA_ERR_TIMEOUT if a bounded wait ran out, DSA_ERR_BOUNDS if a kernel skipped an

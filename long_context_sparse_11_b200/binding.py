@@ -9,12 +9,13 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdsa.so")
 
-DSA_BF16, DSA_E4M3 = 0, 1
+DSA_BF16, DSA_E4M3, DSA_MXFP4, DSA_F16, DSA_F32 = 0, 1, 2, 3, 4
+MXFP4_ROW = 320  # bytes of a 4-bit latent row
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "stale index handle", 4: "device wait timed out",
           5: "CUDA error", 6: "workspace too small", 7: "index or page out of range",
           8: "input value outside the supported range"}
@@ -29,7 +30,8 @@ EXPORTS = [
     "dsa_set_wait_limit_ns", "dsa_launch_count", "dsa_topk_no_alloc", "dsa_cache_write_e4m3",
     "dsa_indexer_project_workspace_bytes", "dsa_indexer_project", "dsa_mla_latent_workspace_bytes", "dsa_mla_latent",
     "dsa_rope_query", "dsa_split_candidates", "dsa_split_merge_workspace_bytes", "dsa_split_merge",
-    "dsa_combine_partials", "dsa_cache_write_e4m3_pools",
+    "dsa_combine_partials", "dsa_cache_write_e4m3_pools", "dsa_rope_plan_init", "dsa_rope", "dsa_latent_append",
+    "dsa_latent_read",
 ]
 
 
@@ -50,6 +52,29 @@ class GroupArgs(ctypes.Structure):
                 ("n_layers", c_int32), ("first_layer", c_int32), ("softmax_scale", c_float),
                 ("q", c_void_p * 4), ("kv", CacheView * 4), ("out", c_void_p * 4), ("lse", c_void_p * 4),
                 ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("trace_events", c_void_p)]
+
+
+class RopePlan(ctypes.Structure):
+    """Which dims of a head turn how far per position (dsa_rope_plan_init): rot_dim of them, paired
+    "interleaved" (2i, 2i + 1) or "half" (i, i + rot_dim / 2), with theta and the angle rule `scaling`: None,
+    "linear", "ntk" or "yarn" (factor; YaRN also original_len, beta_fast, beta_slow).  mscale multiplies the
+    rotated values; by default it is the rule's own."""
+
+    _fields_ = [("inv_freq", c_double * 128), ("mscale", c_double), ("rot_dim", c_int32), ("layout", c_int32)]
+    LAYOUTS = {"interleaved": 0, "half": 1}
+    SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    def __init__(self, rot_dim: int, theta: float = 8.0e6, layout: str = "interleaved", scaling=None,
+                 factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 mscale=None):
+        super().__init__()
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise DsaError(DSA_ERR_INVALID_ARG, f"rope layout {layout!r} / scaling {scaling!r} unknown")
+        if mscale is not None and not mscale > 0:
+            raise DsaError(DSA_ERR_INVALID_ARG, "mscale must be > 0")
+        _check(load().dsa_rope_plan_init(ctypes.byref(self), rot_dim, self.LAYOUTS[layout], theta,
+                                         self.SCALINGS[scaling], factor, original_len, beta_fast, beta_slow,
+                                         0.0 if mscale is None else mscale))
 
 
 class DsaError(RuntimeError):
@@ -109,6 +134,13 @@ def load(path: str = LIB_PATH):
         "dsa_split_merge": (S, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                 c_void_p, c_size_t, c_void_p]),
         "dsa_combine_partials": (S, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+        "dsa_rope_plan_init": (S, [POINTER(RopePlan), c_int32, c_int32, c_double, c_int32, c_double, c_double,
+                                   c_double, c_double, c_double]),
+        "dsa_rope": (S, [POINTER(RopePlan), c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                         c_int64, c_int64, c_int64, c_int64, c_int32, c_void_p]),
+        "dsa_latent_append": (S, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_double, POINTER(RopePlan),
+                                  c_void_p, c_void_p, POINTER(CacheView), c_void_p]),
+        "dsa_latent_read": (S, [POINTER(CacheView), c_void_p, c_void_p, c_int32, c_void_p, c_int64, c_void_p]),
         "dsa_cache_write_e4m3_pools": (S, [c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p,
                                            c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p]),
     }
@@ -133,6 +165,34 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+def _refuse(detail: str):
+    raise DsaError(DSA_ERR_INVALID_ARG, detail)
+
+
+def _on_device(*tensors):
+    """All tensors on the current CUDA device (the library's calls run there, on its current stream)."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            _refuse(f"tensors must be on a CUDA device, got {t.device}")
+        if dev is None:
+            dev = t.device.index
+            if dev != torch.cuda.current_device():
+                _refuse(f"tensor on cuda:{dev}, current device cuda:{torch.cuda.current_device()}")
+        elif t.device.index != dev:
+            _refuse(f"tensors on cuda:{dev} and cuda:{t.device.index}")
+
+
+def _i32(t, n: int, name: str):
+    """A contiguous int32 vector of n entries (or None)."""
+    import torch
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1)):
+        _refuse(f"{name} must be a contiguous int32 tensor of {n} entries")
+
+
 # ------------------------------------------------------------------------------ cache views
 
 
@@ -149,7 +209,9 @@ def dense_view(data, scale=None) -> CacheView:
 
 def paged_view(pool, scale, block_table, seq_lens, rows_per_seq: int = 1) -> CacheView:
     """Paged e4m3 cache: pool [n_pages,64,dim] uint8, scale [n_pages,64] fp32,
-    block_table [B,max_pages] int32, seq_lens [B] int32 (all on the device).
+    block_table [B,max_pages] int32, seq_lens [B] int32 (all on the device).  With scale None: a paged latent
+    cache in 4 bits, pool [n_pages,64,320] uint8 (:func:`latent_pool4`), for the attention of
+    :func:`sparse_mla_attn` and :class:`IndexShareGroup`, :func:`latent_append` and :func:`latent_read`.
 
     rows_per_seq > 1 presents each sequence as that many consecutive entries sharing its pages
     and length (the block-table rows and lengths are repeated once, here; the pages are not
@@ -157,13 +219,35 @@ def paged_view(pool, scale, block_table, seq_lens, rows_per_seq: int = 1) -> Cac
     as its own row, for a per-row Top-k instead of the reuse of row 0's."""
     n_pages, page, dim = pool.shape
     assert page == 64 and rows_per_seq >= 1
+    if scale is None:
+        _check_pool4(pool, block_table, seq_lens)
     if rows_per_seq > 1:
         block_table = block_table.repeat_interleave(rows_per_seq, dim=0).contiguous()
         seq_lens = seq_lens.repeat_interleave(rows_per_seq).contiguous()
+    if scale is None:
+        v = CacheView(pool.data_ptr(), None, block_table.data_ptr(), seq_lens.data_ptr(), MXFP4_ROW, n_pages * 64, 576,
+                      DSA_MXFP4, block_table.shape[1], block_table.shape[0])
+        v._keep = (pool, scale, block_table, seq_lens)
+        return v
     v = CacheView(pool.data_ptr(), scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), dim,
                   n_pages * 64, dim, DSA_E4M3, block_table.shape[1], block_table.shape[0])
     v._keep = (pool, scale, block_table, seq_lens)
     return v
+
+
+def _check_pool4(pool, block_table, seq_lens):
+    import torch
+    if pool.dtype != torch.uint8 or pool.dim() != 3 or pool.shape[2] != MXFP4_ROW or not pool.is_contiguous():
+        _refuse(f"a 4-bit pool is a contiguous uint8 tensor [n_pages, 64, {MXFP4_ROW}]")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        _refuse("block_table must be a contiguous int32 tensor [sequences, max_pages]")
+    _i32(seq_lens, block_table.shape[0], "seq_lens")
+
+
+def latent_pool4(n_pages: int, device="cuda"):
+    """An empty pool of 4-bit latent rows, [n_pages, 64, 320] uint8 zeros (every row reads as zeros)."""
+    import torch
+    return torch.zeros(n_pages, 64, MXFP4_ROW, dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------------------ entry points
@@ -248,11 +332,18 @@ def topk_no_alloc(scores, k: int, out, row_len=None, causal_len0: int = 0, max_l
     return out
 
 
+def sparse_mla_workspace_bytes(n_q: int, k: int, kv: CacheView) -> int:
+    """Bytes of device workspace that :func:`sparse_mla_attn` needs for these sizes (0: none)."""
+    return load().dsa_sparse_mla_workspace_bytes(n_q, k, ctypes.byref(kv))
+
+
 def sparse_mla_attn(q, kv: CacheView, idx, k: int, softmax_scale: float, q_rows_per_idx_row: int = 1,
                     out=None, lse=None, workspace=None):
     """a6: out [n_q,64,512] bf16 and lse [n_q,64] fp32 of sparse MLA over idx."""
     import torch
     n_q = q.shape[0]
+    if kv.dtype == DSA_MXFP4:
+        _check_attn4(q, kv, idx, k, q_rows_per_idx_row, out, lse, workspace)
     out = torch.empty(n_q, 64, 512, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(n_q, 64, dtype=torch.float32, device=q.device) if lse is None else lse
     lib = load()
@@ -263,6 +354,25 @@ def sparse_mla_attn(q, kv: CacheView, idx, k: int, softmax_scale: float, q_rows_
                                    softmax_scale, out.data_ptr(), lse.data_ptr(), _ptr(workspace),
                                    0 if workspace is None else workspace.numel(), _stream()))
     return out, lse
+
+
+def _check_attn4(q, kv, idx, k, rows, out, lse, workspace):
+    """The arguments of attention over a 4-bit cache, before their addresses are passed on."""
+    import torch
+    n = q.shape[0]
+    if q.dtype != torch.bfloat16 or q.shape[1:] != (64, 576) or not q.is_contiguous():
+        _refuse("q must be a contiguous bf16 tensor [n_q, 64, 576]")
+    if rows < 1 or n % rows:
+        _refuse(f"{n} query rows do not divide into groups of {rows}")
+    if idx.dtype != torch.int32 or idx.shape != (n // rows, k) or not idx.is_contiguous():
+        _refuse(f"idx must be a contiguous int32 tensor [{n // rows}, {k}]")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != (n, 64, 512) or not out.is_contiguous()):
+        _refuse("out must be a contiguous bf16 tensor [n_q, 64, 512]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, 64) or not lse.is_contiguous()):
+        _refuse("lse must be a contiguous fp32 tensor [n_q, 64]")
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        _refuse("workspace must be a contiguous uint8 tensor")
+    _on_device(q, kv._keep[0], idx, out, lse, workspace)
 
 
 ROPE_THETA = 8.0e6
@@ -306,6 +416,76 @@ def rope_query(q, pos, theta: float = ROPE_THETA):
     """Turn dims 512..575 of every head of q [T,64,576] bf16 in place to positions pos [T] int32."""
     _check(load().dsa_rope_query(q.data_ptr(), pos.data_ptr(), q.shape[0], theta, _stream()))
     return q
+
+
+def rope(x, pos, plan: RopePlan, offset: int = 0, backward: bool = False, out=None):
+    """Rotary positions: dims offset .. offset + plan.rot_dim of every head of x [T,H,D] or [T,D] (bf16, fp16 or
+    fp32; any token and head strides of whole 16 bytes) turned to positions pos [T] int32, into `out` (a new tensor
+    by default; `out=x` in place).  backward=True is the gradient: rope(grad_out, ..., backward=True) is the
+    gradient of x.  Nothing is recorded for autograd."""
+    import torch
+    dt = {torch.bfloat16: DSA_BF16, torch.float16: DSA_F16, torch.float32: DSA_F32}.get(x.dtype)
+    if dt is None or x.dim() not in (2, 3):
+        _refuse("x must be a bf16, fp16 or fp32 tensor [T, H, D] or [T, D]")
+    if x.requires_grad and torch.is_grad_enabled():
+        _refuse("rope records nothing for autograd: detach x; its gradient is rope(grad, ..., backward=True)")
+    T, D = x.shape[0], x.shape[-1]
+    H = x.shape[1] if x.dim() == 3 else 1
+    _i32(pos, T, "pos")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        _refuse("out must have x's shape and dtype")
+    if D > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1):
+        _refuse("the last dimension must be contiguous")
+    _on_device(x, pos, out)
+    xh, oh = (x.stride(1), out.stride(1)) if x.dim() == 3 else (D, D)
+    if H == 1:  # the stride of a single head is of no account
+        xh = oh = D
+    xt, ot = (x.stride(0), out.stride(0)) if T > 1 else (H * D, H * D)
+    _check(load().dsa_rope(ctypes.byref(plan), x.data_ptr(), out.data_ptr(), dt, pos.data_ptr(), T, H, D, offset, xt, xh,
+                           ot, oh, 1 if backward else 0, _stream()))
+    return out
+
+
+def latent_append(x, pos, cache: CacheView, gamma=None, eps: float = 1e-6, rope=None, seq=None):
+    """New latent rows x [n,576] (bf16 or fp32) into the paged cache `cache` (e4m3 or 4 bits): RMSNorm of the first
+    512 dims times gamma [512] fp32 (none when gamma is None), rotation of the last 64 by `rope` (a RopePlan of 64
+    dims, or None), quantised and stored at position pos[r] of sequence seq[r] (r when seq is None), in one launch.
+    Each (sequence, position) at most once per call."""
+    import torch
+    dt = {torch.bfloat16: DSA_BF16, torch.float32: DSA_F32}.get(x.dtype)
+    if dt is None or x.dim() != 2 or x.shape[1] != 576 or x.stride(1) != 1:
+        _refuse("x must be a bf16 or fp32 tensor [n, 576] with contiguous rows")
+    n = x.shape[0]
+    _i32(pos, n, "pos")
+    _i32(seq, n, "seq")
+    if gamma is not None and (gamma.dtype != torch.float32 or gamma.shape != (512,) or not gamma.is_contiguous()):
+        _refuse("gamma must be a contiguous fp32 tensor of 512 entries")
+    _on_device(x, pos, seq, gamma, cache._keep[0])
+    _check(load().dsa_latent_append(x.data_ptr(), dt, x.stride(0) if n > 1 else 576, n, _ptr(gamma), eps,
+                                    None if rope is None else ctypes.byref(rope), _ptr(seq), pos.data_ptr(),
+                                    ctypes.byref(cache), _stream()))
+    return cache
+
+
+def latent_read(cache: CacheView, pos, seq=None, out=None):
+    """Rows of the paged latent cache `cache` (e4m3 or 4 bits) back as bf16 [n,576]: position pos[r] of sequence
+    seq[r] (r when seq is None)."""
+    import torch
+    if pos.dim() != 1:
+        _refuse("pos must be a vector")
+    n = pos.shape[0]
+    _i32(pos, n, "pos")
+    _i32(seq, n, "seq")
+    if out is None:
+        out = torch.empty(n, 576, dtype=torch.bfloat16, device=pos.device)
+    elif out.dtype != torch.bfloat16 or out.shape != (n, 576) or out.stride(1) != 1:
+        _refuse("out must be a bf16 tensor [n, 576] with contiguous rows")
+    _on_device(pos, seq, out, cache._keep[0])
+    _check(load().dsa_latent_read(ctypes.byref(cache), _ptr(seq), pos.data_ptr(), n, out.data_ptr(),
+                                  out.stride(0) if n > 1 else 576, _stream()))
+    return out
 
 
 def split_candidates(scores, idx_local, n_local: int, offset: int):

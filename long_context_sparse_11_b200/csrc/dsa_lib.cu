@@ -19,9 +19,12 @@
 #include "../../include/dsa.h"
 #include "gemm.cuh"
 #include "indexer.cuh"
+#include "latent4.cuh"
 #include "mla.cuh"
+#include "mla4.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "rope.cuh"
 #include "splitn.cuh"
 #include "topk.cuh"
 
@@ -154,6 +157,9 @@ dsa_status device_state(DeviceState** out) {
     DSA_TRY(cuda_check(cudaFuncSetAttribute(mla::sparse_mla_kernel<true, true>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize, mla::SMEM_BYTES),
                        "smem attr"));
+    DSA_TRY(cuda_check(cudaFuncSetAttribute(mla4::sparse_mla4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            mla4::SMEM_BYTES),
+                       "smem attr"));
     DSA_TRY(cuda_check(cudaFuncSetAttribute(gemm::gemm_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             gemm::SMEM_BYTES),
                        "smem attr"));
@@ -204,6 +210,17 @@ dsa_status check_view(const dsa_cache_view* v, int32_t dim, const char* name) {
   if (!v) return fail(DSA_ERR_INVALID_ARG, "%s: null cache view", name);
   if (!v->data || !aligned16(v->data)) return fail(DSA_ERR_INVALID_ARG, "%s: data null or not 16-byte aligned", name);
   if (v->dim != dim) return fail(DSA_ERR_UNSUPPORTED, "%s: dim %d, expected %d", name, v->dim, dim);
+  if (v->dtype == DSA_MXFP4) {
+    if (dim != DSA_DQK || !v->block_table)
+      return fail(DSA_ERR_UNSUPPORTED, "%s: 4-bit caches must be paged latent caches", name);
+    if (v->scale) return fail(DSA_ERR_INVALID_ARG, "%s: a 4-bit cache holds its exponents itself (scale must be null)", name);
+    if (v->row_stride != DSA_MXFP4_ROW) return fail(DSA_ERR_INVALID_ARG, "%s: 4-bit row_stride must be %d", name, DSA_MXFP4_ROW);
+    if (!v->seq_lens) return fail(DSA_ERR_INVALID_ARG, "%s: paged cache needs seq_lens", name);
+    if (v->max_pages <= 0 || v->batch <= 0) return fail(DSA_ERR_INVALID_ARG, "%s: bad max_pages/batch", name);
+    if (v->n_tokens < 0 || v->n_tokens % DSA_PAGE || v->n_tokens > INT32_MAX)
+      return fail(DSA_ERR_INVALID_ARG, "%s: n_tokens must be pages*64, below 2^31", name);
+    return DSA_OK;
+  }
   if (v->dtype != DSA_BF16 && v->dtype != DSA_E4M3) return fail(DSA_ERR_INVALID_ARG, "%s: bad dtype", name);
   const int64_t es = v->dtype == DSA_BF16 ? 2 : 1;
   if (v->n_tokens < 0) return fail(DSA_ERR_INVALID_ARG, "%s: n_tokens < 0", name);
@@ -221,6 +238,23 @@ dsa_status check_view(const dsa_cache_view* v, int32_t dim, const char* name) {
       return fail(DSA_ERR_INVALID_ARG, "%s: row_stride %lld invalid", name, static_cast<long long>(v->row_stride));
     if (v->n_tokens > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "%s: n_tokens too large", name);
   }
+  return DSA_OK;
+}
+
+// The paged latent cache of an append or a read (an append does not read seq_lens).
+dsa_status check_latent_pages(const dsa_cache_view* v) {
+  if (!v) return fail(DSA_ERR_INVALID_ARG, "cache: null cache view");
+  if (!v->block_table) return fail(DSA_ERR_UNSUPPORTED, "cache: must be paged");
+  dsa_cache_view c = *v;
+  if (!c.seq_lens) c.seq_lens = c.block_table;  // only so that the common check passes
+  return check_view(&c, DSA_DQK, "cache");
+}
+
+dsa_status check_rope_plan(const dsa_rope_plan* p) {
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "null rope plan");
+  if (p->rot_dim < 16 || p->rot_dim > 2 * DSA_ROPE_MAX_PAIRS || p->rot_dim % 16 ||
+      (p->layout != DSA_ROPE_INTERLEAVED && p->layout != DSA_ROPE_HALF))
+    return fail(DSA_ERR_INVALID_ARG, "rope plan not initialised by dsa_rope_plan_init");
   return DSA_OK;
 }
 
@@ -409,12 +443,41 @@ bool mla_query_prepass(int32_t n_q, int32_t k, int sms) {
   return cuts >= 8;
 }
 
+dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* idx, int32_t n_q, int32_t rpi,
+                       int32_t k, float softmax_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                       cudaStream_t st) {
+  DeviceState* ds = nullptr;
+  DSA_TRY(device_state(&ds));
+  (void)ws, (void)ws_bytes;
+  mla4::Params p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv->data);
+  p.block_table = kv->block_table;
+  p.seq_lens = kv->seq_lens;
+  p.idx = idx;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.n_q = n_q;
+  p.rows_per_idx = rpi;
+  p.k = k;
+  p.batch = kv->batch;
+  p.max_pages = kv->max_pages;
+  p.n_pages = static_cast<int32_t>(kv->n_tokens / DSA_PAGE);
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.status = ds->status;
+  launch_pdl(mla4::sparse_mla4_kernel, dim3(static_cast<unsigned>(n_q), 64 / mla4::HPC), mla4::THREADS,
+             mla4::SMEM_BYTES, st, p);
+  count_launch();
+  return cuda_check(cudaGetLastError(), "4-bit sparse MLA launch");
+}
+
 dsa_status launch_mla(const void* q, const dsa_cache_view* kv, const int32_t* idx, int32_t n_q, int32_t rpi,
                       int32_t k, float softmax_scale, void* out, float* lse, void* ws, size_t ws_bytes,
                       cudaStream_t st, int64_t valid0 = -1, const void* q16 = nullptr) {
   DeviceState* ds = nullptr;
   DSA_TRY(device_state(&ds));
   if (n_q == 0) return DSA_OK;
+  if (kv->dtype == DSA_MXFP4) return launch_mla4(q, kv, idx, n_q, rpi, k, softmax_scale, out, lse, ws, ws_bytes, st);
   const bool paged = kv->block_table != nullptr;
   mla::Params p{};
   p.q = static_cast<const uint16_t*>(q);
@@ -590,7 +653,7 @@ dsa_status plan_group(const dsa_group_args* a, int sms, GroupPlan* g) {
   const int32_t nq = a->n_idx_rows * a->q_rows_per_idx_row;
   mla_ws = mla_ws_bytes(nq, a->k, sms);
   int n_paged = 0;
-  for (int l = 0; l < a->n_layers; ++l) n_paged += a->kv[l].block_table != nullptr;
+  for (int l = 0; l < a->n_layers; ++l) n_paged += a->kv[l].dtype == DSA_E4M3;
   if (n_paged > 0 && mla_query_prepass(nq, a->k, sms)) {
     g->q16_layer_bytes = static_cast<size_t>(nq) * 64 * 576 * 2;
     g->off_q16 = take(g->q16_layer_bytes * n_paged);
@@ -645,6 +708,7 @@ size_t dsa_abi_sizeof(int32_t which) {
     case 0: return sizeof(dsa_cache_view);
     case 1: return sizeof(dsa_index_handle);
     case 2: return sizeof(dsa_group_args);
+    case 3: return sizeof(dsa_rope_plan);
   }
   return 0;
 }
@@ -901,6 +965,202 @@ dsa_status dsa_split_merge(const float* cand_score, const int32_t* cand_idx, int
   return cuda_check(cudaGetLastError(), "split map launch");
 }
 
+dsa_status dsa_rope_plan_init(dsa_rope_plan* plan, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                              double factor, double original_len, double beta_fast, double beta_slow, double mscale) {
+  if (!plan) return fail(DSA_ERR_INVALID_ARG, "null rope plan");
+  if (rot_dim < 16 || rot_dim > 2 * DSA_ROPE_MAX_PAIRS || rot_dim % 16)
+    return fail(DSA_ERR_UNSUPPORTED, "rot_dim %d (a multiple of 16, at most %d)", rot_dim, 2 * DSA_ROPE_MAX_PAIRS);
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF) return fail(DSA_ERR_INVALID_ARG, "bad rope layout");
+  if (scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN) return fail(DSA_ERR_INVALID_ARG, "bad rope scaling");
+  if (!(theta > 1.0) || !std::isfinite(theta)) return fail(DSA_ERR_INVALID_ARG, "theta must be finite and > 1");
+  if (scaling != DSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(DSA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (scaling == DSA_ROPE_YARN && (!(original_len > 0.0) || !std::isfinite(original_len) || !(beta_slow > 0.0) ||
+                                   !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+    return fail(DSA_ERR_INVALID_ARG, "YaRN needs original_len > 0 and beta_fast >= beta_slow > 0");
+  if (!std::isfinite(mscale)) return fail(DSA_ERR_INVALID_ARG, "mscale must be finite");
+  const double d = rot_dim, pi = 3.14159265358979323846;
+  const double base = scaling == DSA_ROPE_NTK ? theta * std::pow(factor, d / (d - 2.0)) : theta;
+  double low = 0.0, high = 0.0;
+  if (scaling == DSA_ROPE_YARN) {
+    auto dim_of = [&](double turns) {
+      return d * std::log(original_len / (turns * 2.0 * pi)) / (2.0 * std::log(theta));
+    };
+    low = std::max(std::floor(dim_of(beta_fast)), 0.0);
+    high = std::min(std::ceil(dim_of(beta_slow)), d - 1.0);
+  }
+  std::memset(plan, 0, sizeof(*plan));
+  plan->rot_dim = rot_dim;
+  plan->layout = layout;
+  plan->mscale = mscale > 0.0 ? mscale : scaling == DSA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / d);
+    if (scaling == DSA_ROPE_LINEAR) f /= factor;
+    if (scaling == DSA_ROPE_YARN) {
+      // high <= low: the ramp is a step at low
+      const double g = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      f = f * (1.0 - g) + f / factor * g;
+    }
+    plan->inv_freq[i] = f;
+  }
+  return DSA_OK;
+}
+
+dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t dtype, const int32_t* pos,
+                    int32_t n_tokens, int32_t n_heads, int32_t dim, int32_t offset, int64_t x_token_stride,
+                    int64_t x_head_stride, int64_t out_token_stride, int64_t out_head_stride, int32_t backward,
+                    void* stream) {
+  DSA_TRY(check_rope_plan(plan));
+  if (dtype != DSA_BF16 && dtype != DSA_F16 && dtype != DSA_F32)
+    return fail(DSA_ERR_UNSUPPORTED, "rope dtype must be bf16, f16 or f32");
+  if (n_tokens < 0 || n_heads < 0) return fail(DSA_ERR_INVALID_ARG, "negative size");
+  const int64_t v = dtype == DSA_F32 ? 4 : 8;  // elements of 16 bytes
+  if (offset < 0 || dim <= 0 || offset > dim - plan->rot_dim)
+    return fail(DSA_ERR_INVALID_ARG, "rotated dims [%d, %d) outside a head of %d", offset, offset + plan->rot_dim, dim);
+  if (offset % v || dim % v) return fail(DSA_ERR_INVALID_ARG, "offset and dim must be multiples of 16 bytes");
+  if (n_tokens == 0 || n_heads == 0) return DSA_OK;
+  if (!x || !aligned16(x) || !out || !aligned16(out) || !pos)
+    return fail(DSA_ERR_INVALID_ARG, "x / out / pos null or misaligned");
+  if (x_token_stride % v || x_head_stride % v || out_token_stride % v || out_head_stride % v)
+    return fail(DSA_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+  if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return fail(DSA_ERR_INVALID_ARG, "in place: out's strides must be x's");
+  // a row of out that another one overlaps would be turned twice or torn
+  if ((n_heads > 1 && out_head_stride < dim) ||
+      (n_tokens > 1 && out_token_stride < (n_heads - 1) * out_head_stride + dim &&
+       !(n_heads > 1 && out_head_stride >= (n_tokens - 1) * out_token_stride + dim && out_token_stride >= dim)))
+    return fail(DSA_ERR_INVALID_ARG, "out's tokens or heads overlap");
+  DeviceState* ds = nullptr;
+  DSA_TRY(device_state(&ds));
+  rope::Params p{};
+  p.x = static_cast<const uint8_t*>(x);
+  p.out = static_cast<uint8_t*>(out);
+  p.pos = pos;
+  p.x_tok = x_token_stride, p.x_head = x_head_stride;
+  p.out_tok = out_token_stride, p.out_head = out_head_stride;
+  p.n_tokens = n_tokens, p.n_heads = n_heads, p.dim = dim, p.offset = offset, p.rot = plan->rot_dim;
+  p.half = plan->layout == DSA_ROPE_HALF;
+  p.copy_rest = x != out;
+  p.sin_sign = backward ? -1.0 : 1.0;
+  p.mscale = plan->mscale;
+  rope::Freqs fr;
+  std::memcpy(fr.f, plan->inv_freq, sizeof(fr.f));
+  // 16-byte steps of one head; enough of them per CTA to pay for its sines and cosines, few enough to fill the SMs
+  const int64_t per_head = (p.half ? p.rot / 2 : p.rot) / v + (p.copy_rest ? (dim - p.rot) / v : 0);
+  const int64_t total = per_head * n_heads * n_tokens;
+  const int64_t want = std::min<int64_t>(std::max<int64_t>(total / (4LL * ds->sms), rope::THREADS), 8 * rope::THREADS);
+  const int64_t per_tok = per_head * n_heads;
+  if (per_tok >= want) {
+    p.tok_per_cta = 1;
+    p.head_per_cta = static_cast<int32_t>(std::min<int64_t>(n_heads, (want + per_head - 1) / per_head));
+  } else {
+    p.tok_per_cta = static_cast<int32_t>(std::min<int64_t>(32, (want + per_tok - 1) / per_tok));
+    p.head_per_cta = n_heads;
+  }
+  p.head_groups = (n_heads + p.head_per_cta - 1) / p.head_per_cta;
+  const int64_t grid = (static_cast<int64_t>(n_tokens) + p.tok_per_cta - 1) / p.tok_per_cta * p.head_groups;
+  if (grid > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many tokens x heads");
+  const size_t smem = static_cast<size_t>(p.tok_per_cta) * (p.rot / 2) * sizeof(float2);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 g(static_cast<unsigned>(grid));
+  if (dtype == DSA_BF16)
+    launch_pdl(rope::rope_kernel<__nv_bfloat16>, g, rope::THREADS, smem, st, p, fr);
+  else if (dtype == DSA_F16)
+    launch_pdl(rope::rope_kernel<__half>, g, rope::THREADS, smem, st, p, fr);
+  else
+    launch_pdl(rope::rope_kernel<float>, g, rope::THREADS, smem, st, p, fr);
+  count_launch();
+  return cuda_check(cudaGetLastError(), "rope launch");
+}
+
+dsa_status dsa_latent_append(const void* x, int32_t x_dtype, int64_t x_stride, int32_t n_rows, const float* gamma,
+                             double eps, const dsa_rope_plan* rope, const int32_t* seq, const int32_t* pos,
+                             const dsa_cache_view* cache, void* stream) {
+  DSA_TRY(check_latent_pages(cache));
+  if (x_dtype != DSA_BF16 && x_dtype != DSA_F32) return fail(DSA_ERR_UNSUPPORTED, "rows must be bf16 or f32");
+  if (n_rows < 0) return fail(DSA_ERR_INVALID_ARG, "n_rows < 0");
+  if (rope) {
+    DSA_TRY(check_rope_plan(rope));
+    if (rope->rot_dim != lat::ROT) return fail(DSA_ERR_UNSUPPORTED, "latent rows rotate %d dims", lat::ROT);
+  }
+  if (gamma && (!(eps >= 0.0) || !std::isfinite(eps))) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (x_stride < lat::DIM || x_stride % (x_dtype == DSA_F32 ? 4 : 8))
+    return fail(DSA_ERR_INVALID_ARG, "x_stride %lld invalid", static_cast<long long>(x_stride));
+  if (n_rows == 0) return DSA_OK;
+  if (!x || !aligned16(x) || !pos) return fail(DSA_ERR_INVALID_ARG, "x / pos null or misaligned");
+  DeviceState* ds = nullptr;
+  DSA_TRY(device_state(&ds));
+  lat::AppendParams p{};
+  p.x = static_cast<const uint8_t*>(x);
+  p.x_stride = x_stride;
+  p.gamma = gamma;
+  p.eps = eps;
+  p.seq = seq;
+  p.pos = pos;
+  p.block_table = cache->block_table;
+  p.pool = static_cast<uint8_t*>(const_cast<void*>(cache->data));
+  p.scale = const_cast<float*>(cache->scale);
+  p.status = ds->status;
+  p.n_rows = n_rows;
+  p.batch = cache->batch;
+  p.max_pages = cache->max_pages;
+  p.n_pages = static_cast<int32_t>(cache->n_tokens / DSA_PAGE);
+  lat::RotFreqs fr{};
+  if (rope) {
+    p.rotate = 1;
+    p.half = rope->layout == DSA_ROPE_HALF;
+    p.mscale = rope->mscale;
+    std::memcpy(fr.f, rope->inv_freq, sizeof(fr.f));
+  }
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + 7) / 8);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = x_dtype == DSA_F32, mx = cache->dtype == DSA_MXFP4;
+  if (f32 && mx)
+    launch_pdl(lat::latent_append_kernel<true, true>, grid, 256, 0, st, p, fr);
+  else if (f32)
+    launch_pdl(lat::latent_append_kernel<true, false>, grid, 256, 0, st, p, fr);
+  else if (mx)
+    launch_pdl(lat::latent_append_kernel<false, true>, grid, 256, 0, st, p, fr);
+  else
+    launch_pdl(lat::latent_append_kernel<false, false>, grid, 256, 0, st, p, fr);
+  count_launch();
+  return cuda_check(cudaGetLastError(), "latent append launch");
+}
+
+dsa_status dsa_latent_read(const dsa_cache_view* cache, const int32_t* seq, const int32_t* pos, int32_t n_rows,
+                           void* out_bf16, int64_t out_stride, void* stream) {
+  DSA_TRY(check_latent_pages(cache));
+  if (!cache->seq_lens) return fail(DSA_ERR_INVALID_ARG, "cache: paged cache needs seq_lens");
+  if (n_rows < 0) return fail(DSA_ERR_INVALID_ARG, "n_rows < 0");
+  if (out_stride < lat::DIM || out_stride % 8) return fail(DSA_ERR_INVALID_ARG, "out_stride %lld invalid", static_cast<long long>(out_stride));
+  if (n_rows == 0) return DSA_OK;
+  if (!pos || !out_bf16 || !aligned16(out_bf16)) return fail(DSA_ERR_INVALID_ARG, "pos / out null or misaligned");
+  DeviceState* ds = nullptr;
+  DSA_TRY(device_state(&ds));
+  lat::ReadParams p{};
+  p.pool = static_cast<const uint8_t*>(cache->data);
+  p.scale = cache->scale;
+  p.block_table = cache->block_table;
+  p.seq_lens = cache->seq_lens;
+  p.seq = seq;
+  p.pos = pos;
+  p.out = static_cast<uint16_t*>(out_bf16);
+  p.out_stride = out_stride;
+  p.status = ds->status;
+  p.n_rows = n_rows;
+  p.batch = cache->batch;
+  p.max_pages = cache->max_pages;
+  p.n_pages = static_cast<int32_t>(cache->n_tokens / DSA_PAGE);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + 3) / 4);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cache->dtype == DSA_MXFP4)
+    launch_pdl(lat::latent_read_kernel<true>, grid, 288, 0, st, p);
+  else
+    launch_pdl(lat::latent_read_kernel<false>, grid, 288, 0, st, p);
+  count_launch();
+  return cuda_check(cudaGetLastError(), "latent read launch");
+}
+
 dsa_status dsa_combine_partials(const void* o_parts, const float* lse_parts, int32_t n_parts, int32_t n_q, void* out,
                                 float* lse, void* stream) {
   if (n_parts < 1 || n_q < 0) return fail(DSA_ERR_INVALID_ARG, "bad sizes");
@@ -1058,7 +1318,7 @@ dsa_status indexshare_group_forward(const dsa_group_args* a, dsa_index_handle* h
     mla::QConvert qc{};
     int y = 0;
     for (int l = 0; l < a->n_layers; ++l) {
-      if (!a->kv[l].block_table) continue;
+      if (a->kv[l].dtype != DSA_E4M3) continue;
       qc.src[y] = static_cast<const uint4*>(a->q[l]);
       qc.dst[y] = reinterpret_cast<uint4*>(ws + g.off_q16 + y * g.q16_layer_bytes);
       q16[l] = qc.dst[y];
