@@ -443,12 +443,32 @@ bool mla_query_prepass(int32_t n_q, int32_t k, int sms) {
   return cuts >= 8;
 }
 
+// The 4-bit attention's schedule: equal contiguous tile ranges over one CTA per SM.
+struct Plan4 {
+  int32_t tiles_per_row = 0, grid = 0;
+  int64_t tiles = 0;
+  size_t ws = 0;  // partials of the rows that range boundaries cut, 0 when none does
+};
+Plan4 plan_mla4(int32_t n_q, int32_t k, int sms) {
+  Plan4 pl;
+  if (n_q <= 0 || k <= 0) return pl;
+  pl.tiles_per_row = (k + mla4::TILE - 1) / mla4::TILE;
+  pl.tiles = static_cast<int64_t>(n_q) * pl.tiles_per_row;
+  pl.grid = static_cast<int32_t>(std::min<int64_t>(pl.tiles, sms));
+  for (int32_t c = 1; c < pl.grid; ++c)
+    if ((c * pl.tiles / pl.grid) % pl.tiles_per_row) pl.ws = static_cast<size_t>(pl.grid) * 2 * (64 * 512 + 128) * 4;
+  return pl;
+}
+
 dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* idx, int32_t n_q, int32_t rpi,
                        int32_t k, float softmax_scale, void* out, float* lse, void* ws, size_t ws_bytes,
                        cudaStream_t st) {
   DeviceState* ds = nullptr;
   DSA_TRY(device_state(&ds));
-  (void)ws, (void)ws_bytes;
+  const Plan4 pl = plan_mla4(n_q, k, ds->sms);
+  if (pl.tiles > INT32_MAX - 1024) return fail(DSA_ERR_INVALID_ARG, "too many query rows");
+  if (pl.ws > 0 && (!ws || ws_bytes < pl.ws || !aligned16(ws)))
+    return fail(DSA_ERR_WORKSPACE, "4-bit sparse MLA needs %zu workspace bytes (16-byte aligned)", pl.ws);
   mla4::Params p{};
   p.q = static_cast<const uint16_t*>(q);
   p.kv = static_cast<const uint8_t*>(kv->data);
@@ -457,18 +477,29 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   p.idx = idx;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = p.part_o + static_cast<size_t>(pl.grid) * 2 * 64 * 512;
   p.n_q = n_q;
   p.rows_per_idx = rpi;
   p.k = k;
   p.batch = kv->batch;
   p.max_pages = kv->max_pages;
   p.n_pages = static_cast<int32_t>(kv->n_tokens / DSA_PAGE);
+  p.tiles = static_cast<int32_t>(pl.tiles);
+  p.tiles_per_row = pl.tiles_per_row;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = ds->status;
-  launch_pdl(mla4::sparse_mla4_kernel, dim3(static_cast<unsigned>(n_q), 64 / mla4::HPC), mla4::THREADS,
-             mla4::SMEM_BYTES, st, p);
+  p.wait_ns = static_cast<uint64_t>(g_wait_ns);
+  launch_pdl(mla4::sparse_mla4_kernel, dim3(static_cast<unsigned>(pl.grid)), mla4::THREADS, mla4::SMEM_BYTES, st, p);
   count_launch();
-  return cuda_check(cudaGetLastError(), "4-bit sparse MLA launch");
+  DSA_TRY(cuda_check(cudaGetLastError(), "4-bit sparse MLA launch"));
+  if (pl.ws > 0) {
+    launch_pdl(mla4::combine4_kernel, dim3(static_cast<unsigned>(pl.grid - 1), 16), mla4::COMBINE_THREADS, 0, st,
+               p.part_o, p.part_ml, p.tiles_per_row, p.tiles, pl.grid, p.out, p.lse);
+    count_launch();
+    DSA_TRY(cuda_check(cudaGetLastError(), "4-bit combine launch"));
+  }
+  return DSA_OK;
 }
 
 dsa_status launch_mla(const void* q, const dsa_cache_view* kv, const int32_t* idx, int32_t n_q, int32_t rpi,
@@ -652,6 +683,8 @@ dsa_status plan_group(const dsa_group_args* a, int sms, GroupPlan* g) {
   size_t mla_ws = 0;
   const int32_t nq = a->n_idx_rows * a->q_rows_per_idx_row;
   mla_ws = mla_ws_bytes(nq, a->k, sms);
+  for (int l = 0; l < a->n_layers; ++l)
+    if (a->kv[l].dtype == DSA_MXFP4) mla_ws = std::max(mla_ws, plan_mla4(nq, a->k, sms).ws);
   int n_paged = 0;
   for (int l = 0; l < a->n_layers; ++l) n_paged += a->kv[l].dtype == DSA_E4M3;
   if (n_paged > 0 && mla_query_prepass(nq, a->k, sms)) {
@@ -1196,10 +1229,9 @@ dsa_status dsa_topk(const float* scores, int64_t ld, int32_t n_rows, const int32
 }
 
 size_t dsa_sparse_mla_workspace_bytes(int32_t n_q, int32_t k, const dsa_cache_view* kv) {
-  (void)kv;
   DeviceState* ds = nullptr;
   if (device_state(&ds) != DSA_OK) return 0;
-  return mla_ws_bytes(n_q, k, ds->sms);
+  return kv && kv->dtype == DSA_MXFP4 ? plan_mla4(n_q, k, ds->sms).ws : mla_ws_bytes(n_q, k, ds->sms);
 }
 
 dsa_status dsa_sparse_mla_attn(const void* q, const dsa_cache_view* kv, const int32_t* idx, int32_t n_q,
