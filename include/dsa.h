@@ -85,8 +85,8 @@ typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_MXFP4 = 2, DSA_F16 = 3, DSA_F32 =
  *          +-{0, .5, 1, 1.5, 2, 3, 4, 6} (e2m1, 4 bits) and e its block's exponent, -13 <= e <= 13.
  *          Bytes 0..287: 72 little-endian 32-bit words of 8 values; bits 4i..4i+2 of a word are the
  *          magnitude code of value i, bit 8i + 7 is the sign of value i for i < 4, bit 8i + 3 the sign
- *          of value 4 + i.  Bytes 288..305: e + 127 of blocks 0..17 (255: every value of the block is
- *          NaN; other bytes outside 114..140 are read as the nearer end).  Bytes 306..319 are zero.
+ *          of value 4 + i.  Bytes 288..305: e + 127 of blocks 0..17; 141 with 32 codes 7: every value of
+ *          the block is NaN; other bytes outside 114..140 have no meaning.  Bytes 306..319 are zero.
  */
 typedef struct {
   const void* data;

@@ -485,8 +485,9 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   p.batch = kv->batch;
   p.max_pages = kv->max_pages;
   p.n_pages = static_cast<int32_t>(kv->n_tokens / DSA_PAGE);
-  p.tiles = static_cast<int32_t>(pl.tiles);
   p.tiles_per_row = pl.tiles_per_row;
+  p.quot = static_cast<int32_t>(pl.tiles / pl.grid);
+  p.rem = static_cast<int32_t>(pl.tiles % pl.grid);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = ds->status;
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
@@ -494,8 +495,10 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   count_launch();
   DSA_TRY(cuda_check(cudaGetLastError(), "4-bit sparse MLA launch"));
   if (pl.ws > 0) {
-    launch_pdl(mla4::combine4_kernel, dim3(static_cast<unsigned>(pl.grid - 1), 16), mla4::COMBINE_THREADS, 0, st,
-               p.part_o, p.part_ml, p.tiles_per_row, p.tiles, pl.grid, p.out, p.lse);
+    const int32_t by_row = n_q < pl.grid - 1 ? 1 : 0;
+    const dim3 cg(static_cast<unsigned>(by_row ? n_q : pl.grid - 1), 16, 512 / mla4::COMBINE_THREADS);
+    launch_pdl(mla4::combine4_kernel, cg, mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml, p.tiles_per_row, p.quot,
+               p.rem, pl.grid, by_row, p.out, p.lse);
     count_launch();
     DSA_TRY(cuda_check(cudaGetLastError(), "4-bit combine launch"));
   }

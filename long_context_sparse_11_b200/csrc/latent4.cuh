@@ -5,7 +5,9 @@
 // (+-{0, .5, 1, 1.5, 2, 3, 4, 6}) and e the block's exponent, in [-13, 13].
 //   bytes 0..287    72 little-endian words of 8 values: bits 4i..4i+2 of a word = magnitude code of value i,
 //                   bit 8i + 7 = sign of value i (i < 4), bit 8i + 3 = sign of value 4 + i
-//   bytes 288..305  exponent of block b plus 127 (255: a block of NaN), bytes 306..319 zero
+//   bytes 288..305  exponent of block b plus 127, bytes 306..319 zero
+// A block with a NaN is stored as 32 codes 7 with the exponent 14, where code 7 is e5m2's NaN: reading it needs no
+// case of its own.
 // The signs sit where a byte permutation that looks up four magnitudes at once leaves room for them: four values
 // decode with one lookup and one logical operation.  Exponents stay within [-13, 13] so that every value is a
 // normal e5m2 number, which the tensor cores take as it is.
@@ -20,7 +22,7 @@ namespace lat {
 
 constexpr int DIM = 576, NOPE = 512, ROT = 64;
 constexpr int ROW4 = 320, EXP_OFF = 288;
-constexpr int EXP_MIN = -13, EXP_MAX = 13, EXP_NAN = 255;
+constexpr int EXP_MIN = -13, EXP_MAX = 13, EXP_NAN = 14 + 127;
 
 // Physical slot of position t of sequence b, or -1.
 __device__ __forceinline__ int64_t slot_of(int32_t b, int32_t t, const int32_t* block_table, int32_t batch,
@@ -63,18 +65,18 @@ __device__ __forceinline__ uint32_t arrange(uint32_t x) {
 
 // ------------------------------------------------------------------------------------- decoding
 
-// e5m2 bytes of the magnitudes c * 2^e, codes 0..3 in x and 4..7 in y, for an exponent byte of a row.
+// e5m2 bytes of the magnitudes c * 2^e, codes 0..3 in x and 4..7 in y, for an exponent byte of a row: those of
+// exponent 0 with 4 e added to each byte but the zero's.  Two multiply-adds, which leave the ALU to the permutations.
 __device__ __forceinline__ uint2 mag_table(uint32_t exp_byte) {
-  if (exp_byte == EXP_NAN) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const uint32_t k = static_cast<uint32_t>((min(max(static_cast<int>(exp_byte), EXP_MIN + 127), EXP_MAX + 127) - 127) * 4);
-  return make_uint2(0x3E3C3800u + k * 0x01010100u, 0x46444240u + k * 0x01010101u);
+  return make_uint2(exp_byte * 0x04040400u + (0x3E3C3800u - 127u * 0x04040400u),
+                    exp_byte * 0x04040404u + (0x46444240u - 127u * 0x04040404u));
 }
 // The eight values of a word as e5m2 bytes: values 0..3 in x, 4..7 in y.
 __device__ __forceinline__ uint2 word_to_e5m2(uint32_t w, uint2 tab) {
   const uint32_t m = w & 0x77777777u;
   uint2 r;
   r.x = __byte_perm(tab.x, tab.y, m) | (w & 0x80808080u);
-  r.y = __byte_perm(tab.x, tab.y, m >> 16) | ((w << 4) & 0x80808080u);
+  r.y = __byte_perm(tab.x, tab.y, m >> 16) | ((w * 16u) & 0x80808080u);
   return r;
 }
 
@@ -193,6 +195,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
       uint32_t w = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) w |= e2m1_pair(v[i][2 * j] * inv, v[i][2 * j + 1] * inv) << (8 * j);
+      if (bad) w = 0x77777777u;
       *reinterpret_cast<uint32_t*>(dst + (32 * i + lane) * 4) = arrange(w);
     }
     // RoPE dims: interleaved pairs put blocks 16 and 17 on lanes 0-15 and 16-31; halves put block 16 on ra, 17 on rb
@@ -206,7 +209,9 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
     }
     const bool bad_a = ua > 0x7F800000u, bad_b = ub > 0x7F800000u;
     const int ea = bad_a ? 0 : block_exp(__uint_as_float(ua)), eb = bad_b ? 0 : block_exp(__uint_as_float(ub));
-    const uint32_t code = e2m1_pair(ra * exp2_int(-ea), rb * exp2_int(-eb));
+    uint32_t code = e2m1_pair(ra * exp2_int(-ea), rb * exp2_int(-eb));
+    if (bad_a) code = (code & 0xF0u) | 7u;
+    if (bad_b) code = (code & 0x0Fu) | 0x70u;
     if (!p.half) {
       uint32_t w = code << (8 * (lane & 3));
       w |= __shfl_xor_sync(0xffffffffu, w, 1);

@@ -17,7 +17,7 @@
 // a ring, one RoPE sub-tile): S^T of tile j + 1 runs while the softmax of tile j does, and PV of tile j while tile
 // j + 2 is decoded into the sub-tiles it frees.
 //
-// Warps 0..7: softmax and output (warp w: TMEM lane quadrant w % 4, 32 heads from 32 (w / 4)); 8 decode warps: the
+// Warps 0..15: softmax and output (warp w: TMEM lane quadrant w % 4, 16 heads from 16 (w / 4)); 8 decode warps: the
 // query rows, and tile g + 1's 320-byte rows loaded into registers while tile g is decoded; last warp: MMA issuer.
 // CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a range boundary cuts
 // leave fp32 partials for combine4_kernel.
@@ -43,26 +43,32 @@ constexpr int OFF_KR = OFF_KV + SLOTS * SUB;
 constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][128 keys][64 heads]
 constexpr int OFF_MISC = OFF_P + 2 * RSUB;
 constexpr int N_BARS = 6 + SLOTS * 2 + 1;
-constexpr int M_TMEM = 192, M_ABORT = 196;
-constexpr int M_NEED = 200;  // int [4 tiles]: "a head's maximum moved"
-constexpr int M_MASK = 216;  // uint16 [4 tiles][8 warps]: keys that count
+constexpr int M_TMEM = 208, M_ABORT = 212;
+constexpr int M_NEED = 192;  // uint8 [4 head groups][4 tiles]: "a head's maximum moved"
+constexpr int M_MASK = 224;  // uint16 [4 tiles][8 warps]: keys that count
 constexpr int M_ZS = 288;    // float [4 items][64]: logit scale of a head
-constexpr int M_MRUN = M_ZS + 1024;
-constexpr int M_ALPHA = M_MRUN + 256;  // after an item's last tile: the inverse row sums
-constexpr int M_RED = M_ALPHA + 256;   // float [4 quadrants][64]
+constexpr int M_NM = M_ZS + 1024;    // float [64]: BIAS minus the running maximum (log2 units) of a head
+constexpr int M_ALPHA = M_NM + 256;  // float [64]: 2 to the power of its change; after an item's last tile: the
+                                     // inverse row sums
+constexpr int M_RED = M_ALPHA + 256; // float [4 quadrants][64]; the first 64 also take the change of nm
 constexpr int SMEM_BYTES = OFF_MISC + M_RED + 1024;
 static_assert(N_BARS * 8 <= M_TMEM && SMEM_BYTES <= 232448, "shared memory");
 
-constexpr int SM_WARPS = 8, DEC_WARPS = 8, HPW = 32;
+constexpr int SM_WARPS = 16, DEC_WARPS = 8, HPW = 16;
 constexpr int SM_THREADS = SM_WARPS * 32;
+constexpr int Q_WARPS = SM_WARPS + DEC_WARPS;  // warps that split the first query row of a CTA (later ones: the decode warps)
 constexpr int MMA_WARP = SM_WARPS + DEC_WARPS;
-constexpr int THREADS = (MMA_WARP + 1) * 32;
+constexpr int THREADS = (MMA_WARP + 4) * 32;  // seven whole warpgroups (three warps of the last one idle)
+// Registers per thread: 72 at launch for 896 threads; the softmax and the issuer give some of theirs to the decode.
+// Spills would go to L2, since shared memory leaves the L1 cache next to nothing.
+constexpr int REGS_LAUNCH = 72, REGS_SM = 64, REGS_DEC = 96, REGS_MMA = 56;
+static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256;  // S^T buffers at columns 256 and 384; O^T at 0..255
 
 constexpr int B_QFULL = 0, B_SFULL = 1 /* and 2 */, B_PFULL = 3, B_PVDONE = 4, B_RFULL = 5, B_FULL = 6,
               B_EMPTY = B_FULL + SLOTS;
 
-// p is held as 2^(z - m + BIAS): at most 2^(BIAS + GROW) <= 256 (e4m3 ends at 448) while the running maximum m
+// p is held as 2^(z + nm), nm = BIAS - m: at most 2^(BIAS + GROW) <= 256 (e4m3 ends at 448) while the running maximum m
 // trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
 constexpr float BIAS = 4.f, GROW = 4.f;
 
@@ -75,30 +81,29 @@ struct Params {
   uint16_t* out;       // [n_q, 64, 512] bf16
   float* lse;          // [n_q, 64] or null
   // A CTA's range holds at most two cut rows: one begun before it (fragment 0), one that ends after it (fragment 1).
-  float* part_o;       // [grid, 2, 64, 512] fp32
+  float* part_o;       // [grid, 2, 16, 512, 4] fp32 (16 quads of heads, 512 dims, 4 heads)
   float* part_ml;      // [grid, 2, 2, 64] (m in log2 units, l)
   int32_t n_q, rows_per_idx, k, batch, max_pages, n_pages;
-  int32_t tiles, tiles_per_row;  // tiles = n_q * tiles_per_row
+  int32_t tiles_per_row, quot, rem;  // n_q * tiles_per_row = quot * grid + rem
   float scale_log2;
   int* status;
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ uint64_t make_sdesc64(uint32_t saddr) {  // 64-byte swizzle, 8-row groups of 512 bytes
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(512 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)4 << 61;
-  return d;
+// Shared-memory matrix descriptors whose low word is the address / 16 (plus 1 << 16, a leading offset that none of
+// these layouts reads): 128-byte swizzle with 8-row groups of 1,024 bytes, 64-byte swizzle with groups of 512.
+__device__ __forceinline__ uint64_t desc128(uint32_t lo) {
+  return (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+__device__ __forceinline__ uint64_t desc64(uint32_t lo) {
+  return (static_cast<uint64_t>((512u >> 4) | (1u << 14) | (4u << 29)) << 32) | lo;
 }
 // Byte offset of 16-byte chunk c (0..3) of row r inside a 64-byte-swizzled region.
 __device__ __forceinline__ uint32_t sw64_off(uint32_t r, uint32_t c) { return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4); }
 
-// First global tile of CTA c.
-__host__ __device__ __forceinline__ int32_t range_begin(int64_t c, int64_t tiles, int64_t grid) {
-  return static_cast<int32_t>(c * tiles / grid);
+// First global tile of CTA c: floor(c * tiles / grid), with tiles = quot * grid + rem (no 64-bit division).
+__device__ __forceinline__ int32_t range_begin(int32_t c, int32_t quot, int32_t rem, int32_t grid) {
+  return c * quot + c * rem / grid;
 }
 
 // One block of 32 values (16 bytes) to its e5m2 bytes.
@@ -110,32 +115,131 @@ __device__ __forceinline__ void decode32(const uint4& raw, uint32_t exp_byte, ui
   o1 = make_uint4(c.x, c.y, d.x, d.y);
 }
 
-// One query head's 8 bf16 values to 8 e4m3 bytes of the scaled value and 8 of 16 times the rest.
-__device__ __forceinline__ void split_q(const uint4& raw, float mul, bool nan, uint2& hi, uint2& lo) {
+// 8 bf16 values of one query head, scaled by `mul` (a power of two), to 8 e4m3 bytes and 8 of 16 times the rest.
+__device__ __forceinline__ void split_q(const uint4& raw, float mul, uint2& hi, uint2& lo) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t h[4], l[4];
+  const __half2 sixteen = __float2half2_rn(16.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(w[i] << 16) * mul, b = __uint_as_float(w[i] & 0xFFFF0000u) * mul;
-    const __nv_fp8x2_storage_t p = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3);
-    const float ra = (a - __half2float(__ushort_as_half(r.x))) * 16.f, rb = (b - __half2float(__ushort_as_half(r.y))) * 16.f;
-    h[i] = nan ? 0x7F7Fu : p;
-    l[i] = nan ? 0u : __nv_cvt_float2_to_fp8x2(make_float2(ra, rb), __NV_SATFINITE, __NV_E4M3);
+    // exact in f16: 8 significant bits, at most 256 (what lies below f16's range is below 2^-31 of the head's largest)
+    const __half2 v = __floats2half2_rn(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
+    const __half2_raw vr = v;
+    h[i] = __nv_cvt_halfraw2_to_fp8x2(vr, __NV_SATFINITE, __NV_E4M3);
+    const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3);
+    const __half2_raw rest = __hmul2(__hsub2(v, __half2(back)), sixteen);
+    l[i] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
   }
   hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
 }
 
-// Two probabilities to e4m3 bytes (low half of the result) and e5m2 bytes of the rest (high half).
-__device__ __forceinline__ uint32_t split_p(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const __half2_raw hr = h;
-  const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(hr, __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
-  const __half2_raw rest = __hsub2(h, __half2(back));
-  const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E5M2);
-  return hi | (lo << 16);
+// Two fp32 values side by side in a register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four probabilities to e4m3 bytes and e5m2 bytes of the rest.  An e5m2 number is the high byte of an f16: adding half
+// of its last place and taking the high bytes rounds to nearest (ties away from zero), without a conversion.
+__device__ __forceinline__ void split_p(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  const __half2 u = __floats2half2_rn(a, b), v = __floats2half2_rn(c, d);
+  const __half2_raw ur = u, vr = v;
+  const uint32_t hu = __nv_cvt_halfraw2_to_fp8x2(ur, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hv = __nv_cvt_halfraw2_to_fp8x2(vr, __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw bu = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hu), __NV_E4M3);
+  const __half2_raw bv = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hv), __NV_E4M3);
+  const __half2 ru = __hsub2(u, __half2(bu)), rv = __hsub2(v, __half2(bv));
+  hi = __byte_perm(hu, hv, 0x5410);
+  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ru) + 0x00800080u,
+                   *reinterpret_cast<const uint32_t*>(&rv) + 0x00800080u, 0x7531);
+}
+
+// *ptr where `cond` holds, else -1 (and no access).  Nothing waits for the load before its result is used, as it would
+// at the join of a branch.
+__device__ __forceinline__ int32_t load_if(bool cond, const int32_t* ptr) {
+  int32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tmov.b32 %0, -1;\n\t@p ld.global.nc.b32 %0, [%2];\n\t}"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(cond)), "l"(ptr));
+  return r;
+}
+
+// mbar_wait (ptx.cuh) for warps that wait often: each try sleeps until the phase completes or 20 us have passed, where a
+// loop of short tries would take issue slots from the warps that work.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+                                           uint64_t limit_ns) {
+  auto attempt = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (attempt()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!attempt()) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      atomicOr(status, DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // never sleeps
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(count) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_constant__ Params p) {
@@ -147,19 +251,20 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   auto bar = [&](int i) { return bar0 + 8u * i; };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + M_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + M_ABORT);
-  volatile int* need_flags = reinterpret_cast<volatile int*>(misc + M_NEED);
+  volatile uint8_t* need_flags = misc + M_NEED;
   volatile uint16_t* masks = reinterpret_cast<volatile uint16_t*>(misc + M_MASK);
   float* zs = reinterpret_cast<float*>(misc + M_ZS);
-  float* m_run = reinterpret_cast<float*>(misc + M_MRUN);
+  float* nm = reinterpret_cast<float*>(misc + M_NM);
   float* alpha = reinterpret_cast<float*>(misc + M_ALPHA);
   float* red = reinterpret_cast<float*>(misc + M_RED);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* delta = red;  // written by the one thread that has read the head's four maxima
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: a uniform value
   if (base & 1023u) {  // the swizzled layouts need it; the driver places dynamic shared memory so
     if (threadIdx.x == 0) atomicOr(p.status, DEVERR_TIMEOUT);
     return;
   }
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_QFULL), DEC_WARPS);
+    mbar_init(bar(B_QFULL), Q_WARPS);
     mbar_init(bar(B_SFULL), 2);
     mbar_init(bar(B_SFULL + 1), 2);
     mbar_init(bar(B_PFULL), SM_WARPS);
@@ -170,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       mbar_init(bar(B_EMPTY + i), 1);
     }
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) need_flags[i] = 0;
+    for (int i = 0; i < 16; ++i) need_flags[i] = 0;
     fence_mbar_init();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_holder), 512);
@@ -179,91 +284,66 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int32_t tpr = p.tiles_per_row;
-  const int32_t g_begin = range_begin(blockIdx.x, p.tiles, gridDim.x);
-  const int32_t g_end = range_begin(blockIdx.x + 1, p.tiles, gridDim.x);
+  const int32_t g_begin = range_begin(blockIdx.x, p.quot, p.rem, gridDim.x);
+  const int32_t g_end = range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
   const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
 
-  if (warp >= SM_WARPS && warp < MMA_WARP) {
-    // ================================================================= decode warps
-    // Warp dw holds keys 16 dw .. 16 dw + 15 of every tile.  Latent sub-tile d: lane l decodes blocks 4 d + l % 4 of
-    // keys l / 4 and l / 4 + 8 (64 consecutive bytes of a row per four lanes); RoPE: block 16 + l % 2 of key l / 2.
-    const int dw = warp - SM_WARPS;
-    const int c4 = lane & 3, r4 = lane >> 2;
-    auto wait = [&](int b, uint32_t par) {
-      return __all_sync(0xffffffffu, mbar_wait(bar(b), par, abort_flag, p.status, p.wait_ns));
-    };
-    auto publish = [&](int b) {  // this warp's stores are visible to the tensor core, then one arrival
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(b));
-    };
-    // selected position of key 16 dw + lane of tile i (lanes 0..15), -1 past the end
-    auto load_idx = [&](int32_t i) -> int32_t {
-      if (i >= n || lane >= 16) return -1;
-      const int32_t row = (g_begin + i) / tpr, j = (g_begin + i) % tpr;
-      const int32_t at = j * TILE + 16 * dw + lane;
-      return at < p.k ? p.idx[static_cast<int64_t>(row / p.rows_per_idx) * p.k + at] : -1;
-    };
-    auto resolve = [&](int32_t i, int32_t t) -> int32_t {
-      if (t < 0) return -1;
-      const int32_t irow = (g_begin + i) / tpr / p.rows_per_idx;
-      int64_t s = -1;
-      if (t < p.seq_lens[irow]) s = lat::slot_of(irow, t, p.block_table, p.batch, p.max_pages, p.n_pages);
-      if (s < 0) atomicOr(p.status, DEVERR_BOUNDS);
-      return static_cast<int32_t>(s);
-    };
-    uint4 raw[8], raw_r, ex_a, ex_b;
-    uint32_t ex_r;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {
-      const int32_t s = __shfl_sync(0xffffffffu, slot, src);
-      return s < 0 ? nullptr : p.kv + static_cast<int64_t>(s) * lat::ROW4;
-    };
-    auto ld16 = [&](const uint8_t* r, int off) { return r ? __ldg(reinterpret_cast<const uint4*>(r + off)) : zero; };
-
-    // Query row of item `it`: copied as bf16 into the rows that its two parts will fill, then split in place, one
-    // head per step of its warp.
-    auto q_copy = [&](int32_t row) {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152;
-      for (int i = 0; i < 8; ++i) {
-        const int h = dw * 8 + i;
+  // A query row: copied as bf16 into the rows that its two parts will fill, then split in place.  A warp takes heads
+  // h0, h0 + step, ... two at a time, for their latencies.
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto q_copy = [&](int32_t row, int h0, int step) {
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152;
+    for (int h = h0; h < 64; h += step) {
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const int c = lane + 32 * u;
-          if (c < 64) cp_async16(base + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7), src + h * 1152 + c * 16, 16);
-          else if (c < 72) cp_async16(base + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3), src + h * 1152 + c * 16, 16);
-        }
+      for (int u = 0; u < 3; ++u) {
+        const int c = lane + 32 * u;
+        if (c < 64) cp_async16(base + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7), src + h * 1152 + c * 16, 16);
+        else if (c < 72) cp_async16(base + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3), src + h * 1152 + c * 16, 16);
       }
-    };
-    auto q_split = [&](int32_t item) {
-      cp_async_wait_all();
-      __syncwarp();
-      for (int i = 0; i < 8; ++i) {
-        const int h = dw * 8 + i;
-        uint4 v[3];
-        uint32_t amax = 0;
+    }
+  };
+  auto q_split = [&](int32_t item, int h0, int step) {
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll 1
+    for (int h1 = h0; h1 < 64; h1 += 2 * step) {
+      uint4 v[2][3];
+      uint32_t amax[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = min(h1 + e * step, 63);
+        uint32_t am = 0;
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const int c = lane + 32 * u;
-          v[u] = zero;
-          if (c < 64) v[u] = *reinterpret_cast<const uint4*>(smem + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7));
-          else if (c < 72) v[u] = *reinterpret_cast<const uint4*>(smem + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3));
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) amax = max(amax, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+          uint4 x = zero;
+          if (c < 64) x = *reinterpret_cast<const uint4*>(smem + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7));
+          else if (c < 72) x = *reinterpret_cast<const uint4*>(smem + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3));
+          am = max_u16x2(max_u16x2(am, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+          am = max_u16x2(max_u16x2(am, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+          v[e][u] = x;
         }
+        amax[e] = am;
+      }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const bool nan = amax >= 0x7F800000u;  // a head that is not finite becomes NaN throughout
-        int sh = amax == 0u || nan ? 0 : 134 - static_cast<int>(amax >> 23);
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) amax[e] = max_u16x2(amax[e], __shfl_xor_sync(0xffffffffu, amax[e], o));
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = h1 + e * step;
+        if (h >= 64) break;
+        const uint32_t am = max(amax[e] & 0xFFFFu, amax[e] >> 16);  // bf16 bits of the largest magnitude
+        const bool nan = am >= 0x7F80u;  // a head that is not finite becomes NaN throughout
+        int sh = am == 0u || nan ? 0 : 134 - static_cast<int>(am >> 7);
         sh = min(max(sh, -120), 126);
-        const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-        __syncwarp();
+        const float mul = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const int c = lane + 32 * u;
           uint2 hi, lo;
-          split_q(v[u], mul, nan, hi, lo);
+          split_q(v[e][u], mul, hi, lo);
           if (c < 64) {
             uint8_t* d = smem + OFF_Q + (c >> 4) * SUB + (c & 1) * 8;
             *reinterpret_cast<uint2*>(d + sw128_off(h, (c & 15) >> 1)) = hi;
@@ -276,29 +356,91 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         }
         if (lane == 0) zs[(item & 3) * 64 + h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       }
-      publish(B_QFULL);
-    };
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_n(bar(B_QFULL), Q_WARPS / step == 1 ? 1 : Q_WARPS / DEC_WARPS);
+  };
 
-    bool ok = true;
-    if (n > 0) q_copy(g_begin / tpr);
-    int32_t slot = resolve(0, load_idx(0));
-    {
-      const uint8_t *a = row_ptr(slot, r4), *b = row_ptr(slot, r4 + 8), *c = row_ptr(slot, lane >> 1);
+  if (warp >= SM_WARPS && warp < MMA_WARP) {
+    // ================================================================= decode warps
+    regs_inc<REGS_DEC>();
+    // Warp dw holds keys 16 dw .. 16 dw + 15 of every tile.  Latent sub-tile d: lane l decodes blocks 4 d + l % 4 of
+    // keys l / 4 and l / 4 + 8 (64 consecutive bytes of a row per four lanes); RoPE: block 16 + l % 2 of key l / 2.
+    const int dw = warp - SM_WARPS;
+    const int c4 = lane & 3, r4 = lane >> 2;
+    auto wait = [&](int b, uint32_t par) {
+      return __all_sync(0xffffffffu, wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns));
+    };
+    auto publish = [&](int b) {  // this warp's stores are visible to the tensor core, then one arrival
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    // selected position of key 16 dw + lane of tile i (lanes 0..15), -1 past the end
+    auto load_idx = [&](int32_t i) -> int32_t {
+      const int32_t row = (g_begin + i) / tpr, at = (g_begin + i) % tpr * TILE + 16 * dw + lane;
+      return load_if(i < n && lane < 16 && at < p.k, p.idx + static_cast<int64_t>(row / p.rows_per_idx) * p.k + at);
+    };
+    // Its cache slot, in two steps a tile apart, so that no step waits for the load of the one before: the page number
+    // of a position, then the slot (a position or page out of range is reported and skipped).
+    struct Pos {
+      int32_t t, len;  // selected position of key 16 dw + lane (-1: none), the sequence's length
+    };
+    struct Page {
+      int32_t t, page;
+    };
+    auto position = [&](int32_t i) -> Pos {
+      return Pos{load_idx(i), load_if(i < n, p.seq_lens + (g_begin + i) / tpr / p.rows_per_idx)};
+    };
+    auto find_page = [&](int32_t i, const Pos& q) -> Page {
+      const int64_t at = static_cast<int64_t>((g_begin + i) / tpr / p.rows_per_idx) * p.max_pages + (q.t >> 6);
+      return Page{q.t, load_if(q.t >= 0 && q.t < q.len && (q.t >> 6) < p.max_pages, p.block_table + at)};
+    };
+    auto find_slot = [&](const Page& g) -> int32_t {
+      if (g.t < 0) return -1;
+      if (g.page < 0 || g.page >= p.n_pages) {
+        atomicOr(p.status, DEVERR_BOUNDS);
+        return -1;
+      }
+      return g.page * 64 + (g.t & 63);
+    };
+    uint4 raw[8], raw_r, ex_a, ex_b;
+    uint32_t ex_r;
+    auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {
+      const int32_t s = __shfl_sync(0xffffffffu, slot, src);
+      return s < 0 ? nullptr : p.kv + static_cast<int64_t>(s) * lat::ROW4;
+    };
+    auto ld16 = [&](const uint8_t* r, int off) { return r ? __ldg(reinterpret_cast<const uint4*>(r + off)) : zero; };
+
+    auto load = [&](int32_t slots) {
+      const uint8_t *a = row_ptr(slots, r4), *b = row_ptr(slots, r4 + 8), *c = row_ptr(slots, lane >> 1);
+      ex_a = ld16(a, lat::EXP_OFF), ex_b = ld16(b, lat::EXP_OFF);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         raw[2 * d] = ld16(a, d * 64 + c4 * 16);
         raw[2 * d + 1] = ld16(b, d * 64 + c4 * 16);
       }
-      ex_a = ld16(a, lat::EXP_OFF), ex_b = ld16(b, lat::EXP_OFF);
       raw_r = ld16(c, 256 + (lane & 1) * 16);
       ex_r = c ? __ldg(c + lat::EXP_OFF + 16 + (lane & 1)) : 0u;
-    }
-    int32_t slot_next = resolve(1, load_idx(1));
-    int32_t idx_next2 = load_idx(2);
+    };
+
+    auto q_prefetch = [&](int32_t row) {  // 72 lines of this warp's heads
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152 + dw * 8 * 1152;
+      for (int l = lane; l < 72; l += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + l * 128));
+    };
+    bool ok = true;
+    if (n > 0) q_copy(g_begin / tpr, warp, Q_WARPS);
+    const Pos t0 = position(0), t1 = position(1), t2 = position(2);
+    Pos t3 = position(3);  // in the loop: of tile i + 3
+    const Page g0 = find_page(0, t0), g1 = find_page(1, t1);
+    Page g2 = find_page(2, t2);  // of tile i + 2
+    int32_t slot = find_slot(g0), slot_next;
+    load(slot);
+    slot_next = find_slot(g1);
     int32_t item = 0;
-    if (n > 0) q_split(0);
+    if (n > 0) q_split(0, warp, Q_WARPS);
     for (int32_t i = 0; i < n && ok; ++i) {
-      const uint8_t *na = row_ptr(slot_next, r4), *nb = row_ptr(slot_next, r4 + 8), *nc = row_ptr(slot_next, lane >> 1);
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
       const uint32_t xa[4] = {ex_a.x, ex_a.y, ex_a.z, ex_a.w}, xb[4] = {ex_b.x, ex_b.y, ex_b.z, ex_b.w};
 #pragma unroll
@@ -309,23 +451,21 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           if (d == 0 && lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
           uint4 o0, o1;
           uint8_t* dst = smem + OFF_KV + s * SUB;
-          decode32(raw[2 * d], (xa[d] >> (8 * c4)) & 255u, o0, o1);
+          decode32(raw[2 * d], __byte_perm(xa[d], 0, 0x4440u | c4), o0, o1);
           *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4, 2 * c4)) = o0;
           *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4, 2 * c4 + 1)) = o1;
-          decode32(raw[2 * d + 1], (xb[d] >> (8 * c4)) & 255u, o0, o1);
+          decode32(raw[2 * d + 1], __byte_perm(xb[d], 0, 0x4440u | c4), o0, o1);
           *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4 + 8, 2 * c4)) = o0;
           *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4 + 8, 2 * c4 + 1)) = o1;
-          raw[2 * d] = ld16(na, d * 64 + c4 * 16);
-          raw[2 * d + 1] = ld16(nb, d * 64 + c4 * 16);
           publish(B_FULL + s);
         }
       }
-      ex_a = ld16(na, lat::EXP_OFF), ex_b = ld16(nb, lat::EXP_OFF);
       // S^T of the tile before has read its RoPE sub-tile (and its query row)
       if (ok && i >= 1) ok = wait(B_SFULL + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+      if (i + 2 < n && (g_begin + i + 2) % tpr == 0) q_prefetch((g_begin + i + 2) / tpr);
       if (ok && i >= 1 && (g_begin + i) % tpr == 0) {
-        q_copy((g_begin + i) / tpr);
-        q_split(++item);
+        q_copy((g_begin + i) / tpr, dw, DEC_WARPS);
+        q_split(++item, dw, DEC_WARPS);
       }
       if (ok) {
         uint4 o0, o1;
@@ -334,78 +474,120 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         const int r = 16 * dw + (lane >> 1), b = lane & 1;
         *reinterpret_cast<uint4*>(dst + sw64_off(r, 2 * b)) = o0;
         *reinterpret_cast<uint4*>(dst + sw64_off(r, 2 * b + 1)) = o1;
-        raw_r = ld16(nc, 256 + b * 16);
-        ex_r = nc ? __ldg(nc + lat::EXP_OFF + 16 + b) : 0u;
         publish(B_RFULL);
       }
+      load(slot_next);
       slot = slot_next;
-      slot_next = resolve(i + 2, idx_next2);
-      idx_next2 = load_idx(i + 3);
+      slot_next = find_slot(g2);
+      g2 = find_page(i + 3, t3);
+      t3 = position(i + 4);
     }
-  } else if (warp == MMA_WARP) {
+  } else if (warp >= MMA_WARP) {
     // ================================================================= MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);    // e5m2 keys, e4m3 q parts
-      constexpr uint32_t ID_PV[2] = {make_idesc(1, 0, 1, 1, 128, 64),  // e5m2 values, e4m3 p
-                                     make_idesc(1, 1, 1, 1, 128, 64)};  // and the e5m2 rest of p
-      auto wait = [&](int b, uint32_t par) {
-        if (!mbar_wait(bar(b), par, abort_flag, p.status, p.wait_ns)) return false;
-        tc_fence_after();
-        return true;
-      };
-      int32_t item = 0;
-      bool ok = true;
-      for (int32_t i = 0; i <= n && ok; ++i) {
-        if (i < n) {
-          if (i == 0 || (g_begin + i) % tpr == 0) {
-            ok = wait(B_QFULL, item & 1);
-            ++item;
-          }
-          const uint32_t ds = tmem + TM_S + 128u * (i & 1);
-          for (int d = 0; d < 4 && ok; ++d) {
-            const int s = 4 * (i & 1) + d;
-            if (!(ok = wait(B_FULL + s, (i >> 1) & 1))) break;
+    regs_dec<REGS_MMA>();
+    if (warp == MMA_WARP) {
+      // The whole warp runs the loop, and one elected lane issues: every address stays in uniform registers, and an MMA
+      // costs one instruction.  (Issued by one lane of a divergent branch they took 75 to 120 clocks each.)
+      constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);   // e5m2 keys, e4m3 q parts
+      constexpr uint32_t ID_PV = make_idesc(1, 0, 1, 1, 128, 64);   // e5m2 values, e4m3 p
+      constexpr uint32_t ID_PVR = make_idesc(1, 1, 1, 1, 128, 64);  // and the e5m2 rest of p
+      const uint32_t lo0 = (base >> 4) | (1u << 16);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto ready = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_test(bar(b), par)) != 0; };
+      // Two streams of steps, taken as their inputs become ready: S^T of tile `st` (sub-tile `sd` next; 4 = the RoPE dims)
+      // and PV of tile `pt`.  S^T runs up to two tiles ahead of PV.
+      int32_t st = 0, sd = 0, pt = 0, items = 0, row_left = tpr - g_begin % tpr, pv_left = 0;
+      bool q_ready = false, pv_first = true;
+      pv_left = row_left;
+      uint64_t since = 0;
+      while (pt < n) {
+        bool moved = false;
+        if (st < n) {
+          if (!q_ready) q_ready = ready(B_QFULL, items & 1);
+          if (q_ready) {
+            const int s = 4 * (st & 1) + sd;
+            const uint32_t ds = tm + TM_S + 128u * (st & 1);
+            if (sd < 4 ? ready(B_FULL + s, (st >> 1) & 1) : ready(B_RFULL, st & 1)) {
+              tc_fence_after();
+              if (sd < 4) {
+                const uint64_t a = desc128(lo0 + (OFF_KV + s * SUB) / 16), b = desc128(lo0 + (OFF_Q + sd * SUB) / 16);
+                if (elect_one()) {
+                  mma_f8(ds, a, b, ID_S, sd != 0);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8(ds, make_sdesc(base + OFF_KV + s * SUB + kk * 32, 16, 1024),
-                     make_sdesc(base + OFF_Q + d * SUB + kk * 32, 16, 1024), ID_S, (d | kk) != 0);
-          }
-          if (ok) ok = wait(B_RFULL, i & 1);
-          if (!ok) break;
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            mma_f8(ds, make_sdesc64(base + OFF_KR + kk * 32), make_sdesc64(base + OFF_QR + kk * 32), ID_S, 1);
-          mma_commit(bar(B_SFULL + (i & 1)));
-          mbar_arrive(bar(B_SFULL + (i & 1)));  // and what the decode warps left in shared memory (masks, scales)
-        }
-        if (i >= 1) {
-          const int32_t t = i - 1;
-          const bool first = t == 0 || (g_begin + t) % tpr == 0;
-          if (!(ok = wait(B_PFULL, t & 1))) break;
-          for (int mb = 0; mb < 4; ++mb) {
-            const int s = 4 * (t & 1) + mb;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = make_sdesc(base + OFF_KV + s * SUB + kk * 4096, SUB, 1024);
-#pragma unroll
-              for (int u = 0; u < 2; ++u)
-                mma_f8(tmem + 64u * mb, a, make_sdesc64(base + OFF_P + u * RSUB + kk * 2048), ID_PV[u], !first || kk + u > 0);
+                  for (int kk = 1; kk < 4; ++kk) mma_f8(ds, a + 2 * kk, b + 2 * kk, ID_S, 1);
+                }
+                ++sd;
+              } else {
+                const uint64_t a = desc64(lo0 + OFF_KR / 16), b = desc64(lo0 + OFF_QR / 16);
+                if (elect_one()) {
+                  mma_f8(ds, a, b, ID_S, 1);
+                  mma_f8(ds, a + 2, b + 2, ID_S, 1);
+                  mma_commit(bar(B_SFULL + (st & 1)));
+                  mbar_arrive(bar(B_SFULL + (st & 1)));  // and what the decode warps left in shared memory (masks, scales)
+                }
+                sd = 0;
+                ++st;
+                if (--row_left == 0) {
+                  row_left = tpr;
+                  q_ready = false;
+                  ++items;
+                }
+              }
+              moved = true;
             }
-            mma_commit(bar(B_EMPTY + s));
           }
-          mma_commit(bar(B_PVDONE));
+        }
+        if (pt < st && ready(B_PFULL, pt & 1)) {
+          tc_fence_after();
+          const uint64_t a = desc128(lo0 + (OFF_KV + 4 * (pt & 1) * SUB) / 16), b = desc64(lo0 + OFF_P / 16);
+          const uint32_t keep = pv_first ? 0u : 1u;
+          if (elect_one()) {
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {  // 32 keys: 4 groups of 8 rows
+                mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 128 * kk, ID_PV, kk > 0 ? 1u : keep);
+                mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 128 * kk, ID_PVR, 1);
+              }
+              mma_commit(bar(B_EMPTY + 4 * (pt & 1) + mb));
+            }
+            mma_commit(bar(B_PVDONE));
+          }
+          ++pt;
+          pv_first = --pv_left == 0;
+          if (pv_first) pv_left = tpr;
+          moved = true;
+        }
+        __syncwarp();
+        if (moved) {
+          since = 0;
+        } else {  // nothing to issue: bounded like every other wait
+          bool stop = *abort_flag != 0;
+          const uint64_t now = globaltimer_ns();
+          if (since == 0) since = now;
+          if (now - since > p.wait_ns) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(p.status, DEVERR_TIMEOUT);
+            stop = true;
+          }
+          if (__any_sync(0xffffffffu, stop)) break;
         }
       }
     }
   } else {
     // ================================================================= softmax / output warps
+    regs_dec<REGS_SM>();
+    if (n > 0) {
+      q_copy(g_begin / tpr, warp, Q_WARPS);
+      q_split(0, warp, Q_WARPS);
+    }
     const int quad = warp & 3, hh = warp >> 2;
     const int key = quad * 32 + lane;  // TMEM lane: key of S^T, dim of an O^T block
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int hcol = HPW * hh;
     int32_t item = 0;
-    bool ok = true;
-    float lsum[HPW];
+    uint64_t lsum[HPW / 2];
+    bool seen = false;  // the item has had a key that counts (its maxima are set)
     // As in mla.cuh: a failed wait is recorded and acted on at the next named_bar_or, where all softmax threads leave
     // together; before a warp-collective TMEM access the lanes of a warp agree on it.
     bool fail = false;
@@ -413,103 +595,122 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       const int32_t row = (g_begin + i) / tpr, j = (g_begin + i) % tpr;
       const bool first = i == 0 || j == 0, last = i == n - 1 || j == tpr - 1;
       if (first) {
-        if (quad == 0) m_run[hcol + lane] = -INFINITY;
-        named_bar(1, SM_THREADS);
+        if (quad == 0 && lane < HPW) nm[hcol + lane] = BIAS;
+        named_bar(1 + hh, 128);
 #pragma unroll
-        for (int h = 0; h < HPW; ++h) lsum[h] = 0.f;
+        for (int h = 0; h < HPW / 2; ++h) lsum[h] = 0ull;
+        seen = false;
       }
       {
-        const bool got = mbar_wait(bar(B_SFULL + (i & 1)), (i >> 1) & 1, abort_flag, p.status, p.wait_ns);
+        const bool got = wait_phase(bar(B_SFULL + (i & 1)), (i >> 1) & 1, abort_flag, p.status, p.wait_ns);
         fail = __any_sync(0xffffffffu, fail || !got);
       }
       tc_fence_after();
-      const bool valid = (masks[(i & 3) * 8 + (key >> 4)] >> (key & 15)) & 1;
-      float z[HPW];
-      bool exceed = false;
+      const uint4 live = *reinterpret_cast<const uint4*>(misc + M_MASK + (i & 3) * 16);
+      const uint32_t mine = quad == 0 ? live.x : quad == 1 ? live.y : quad == 2 ? live.z : live.w;
+      const bool valid = (mine >> lane) & 1;
+      uint64_t t[HPW / 2];  // log2 of p: s * zs + nm, two heads each
+      float top = -INFINITY;
       if (!fail) {
         const float* zi = zs + (item & 3) * 64 + hcol;
         const uint32_t ts = tmem + TM_S + 128u * (i & 1) + hcol + lane_off;
+        const uint64_t part = pack2(0.0625f, 0.0625f);
+        uint32_t a[HPW], b[HPW];
+        DSA_TMEM_LD_X16_NOWAIT(ts, a);
+        DSA_TMEM_LD_X16_NOWAIT(ts + 64u, b);
+        DSA_TMEM_WAIT_LD_X16(a, b);
 #pragma unroll
-        for (int c = 0; c < HPW / 16; ++c) {
-          uint32_t a[16], b[16];
-          DSA_TMEM_LD_X16(ts + 16u * c, a);
-          DSA_TMEM_LD_X16(ts + 64u + 16u * c, b);
+        for (int h = 0; h < HPW; h += 4) {
+          const ulonglong2 zz = *reinterpret_cast<const ulonglong2*>(zi + h);
+          const ulonglong2 nn = *reinterpret_cast<const ulonglong2*>(nm + hcol + h);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) {
-            const float s = fmaf(__uint_as_float(b[h]), 0.0625f, __uint_as_float(a[h]));
-            z[16 * c + h] = valid ? s * zi[16 * c + h] : -INFINITY;
-            exceed |= z[16 * c + h] > m_run[hcol + 16 * c + h] + GROW;
+          for (int u = 0; u < 2; ++u) {
+            const int e = h + 2 * u;
+            const uint64_t sum = fma2(pack2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])), part,
+                                      pack2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
+            t[e / 2] = fma2(sum, u ? zz.y : zz.x, u ? nn.y : nn.x);
           }
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < HPW; ++h) z[h] = -INFINITY;
+        for (int h = 0; h < HPW / 2; ++h) t[h] = 0ull;
       }
-      volatile int* need = need_flags + (i & 3);
-      if (__any_sync(0xffffffffu, exceed) && lane == 0) *need = 1;
-      if (named_bar_or(1, SM_THREADS, fail)) {
-        ok = false;
-        break;
-      }
-      // a later tile's flag: its last readers have passed this barrier, its next writers wait for the next one
-      if (threadIdx.x == 0) need_flags[(i + 2) & 3] = 0;
-      const bool resc = *need != 0;
-      if (resc) {
-        const float wmax = mla::warp_reduce32<true>(z, lane);
-        red[quad * 64 + hcol + lane] = wmax;
-        named_bar(1, SM_THREADS);
-        if (quad == 0) {
-          const int h = hcol + lane;
-          const float tmax = fmaxf(fmaxf(red[h], red[64 + h]), fmaxf(red[128 + h], red[192 + h]));
-          const float mo = m_run[h];
-          float a = 1.f;
-          if (tmax > -INFINITY && (mo == -INFINITY || tmax > mo + GROW)) {
-            a = mo == -INFINITY ? 0.f : ex2_approx(mo - tmax);
-            m_run[h] = tmax;
-          }
-          alpha[h] = a;
-        }
-        named_bar(1, SM_THREADS);
+      if (mine != 0xFFFFFFFFu) {  // the same in the whole warp
 #pragma unroll
-        for (int h = 0; h < HPW; ++h) lsum[h] *= alpha[hcol + h];
+        for (int h = 0; h < HPW / 2; ++h) t[h] = valid ? t[h] : pack2(-INFINITY, -INFINITY);
       }
+#pragma unroll
+      for (int h = 0; h < HPW / 2; ++h) {
+        const float2 v = unpack2(t[h]);
+        top = fmaxf(top, fmaxf(v.x, v.y));
+      }
+      volatile uint8_t* need = need_flags + 4 * hh + (i & 3);
+      if (__any_sync(0xffffffffu, top > BIAS + GROW) && lane == 0) *need = 1;
+      if (named_bar_or(1 + hh, 128, fail)) break;
+      // a later tile's flag: its last readers have passed this barrier, its next writers wait for the next one
+      if (quad == 0 && lane == 0) need_flags[4 * hh + ((i + 2) & 3)] = 0;
+      const bool resc = *need != 0 || !seen;
+      if (resc) {
+        float v[HPW];
+#pragma unroll
+        for (int h = 0; h < HPW / 2; ++h) {
+          const float2 w = unpack2(t[h]);
+          v[2 * h] = w.x, v[2 * h + 1] = w.y;
+        }
+        const float most = mla::warp_reduce16<true>(v, lane);  // head lane / 2
+        if ((lane & 1) == 0) red[quad * 64 + hcol + lane / 2] = most;
+        named_bar(1 + hh, 128);
+        if (quad == 0 && lane < HPW) {
+          const int h = hcol + lane;
+          const float tmax = fmaxf(fmaxf(red[h], red[64 + h]), fmaxf(red[128 + h], red[192 + h]));  // z + nm
+          float d = 0.f;
+          if (tmax > -INFINITY && (!seen || tmax > BIAS + GROW)) d = BIAS - tmax;
+          delta[h] = d;
+          alpha[h] = seen ? ex2_approx(d) : 0.f;
+          nm[h] += d;
+        }
+        named_bar(1 + hh, 128);
+#pragma unroll
+        for (int h = 0; h < HPW; h += 4) {
+          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(delta + hcol + h);
+          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(alpha + hcol + h);
+          t[h / 2] = add2(t[h / 2], d.x);
+          t[h / 2 + 1] = add2(t[h / 2 + 1], d.y);
+          lsum[h / 2] = mul2(lsum[h / 2], a.x);
+          lsum[h / 2 + 1] = mul2(lsum[h / 2 + 1], a.y);
+        }
+      }
+      const bool rescale_o = resc && seen;
+      seen = seen || (live.x | live.y | live.z | live.w) != 0u;
       uint32_t ph[HPW / 4], pl[HPW / 4];
 #pragma unroll
       for (int h = 0; h < HPW; h += 4) {
-        float e[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float m = m_run[hcol + h + u];
-          e[u] = ex2_approx(z[h + u] - (m == -INFINITY ? 0.f : m) + BIAS);  // 0 for a masked key
-          lsum[h + u] += e[u];
-        }
-        const uint32_t s0 = split_p(e[0], e[1]), s1 = split_p(e[2], e[3]);
-        ph[h / 4] = __byte_perm(s0, s1, 0x5410);
-        pl[h / 4] = __byte_perm(s0, s1, 0x7632);
+        const float2 u = unpack2(t[h / 2]), w = unpack2(t[h / 2 + 1]);
+        const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(w.x), e3 = ex2_approx(w.y);
+        lsum[h / 2] = add2(lsum[h / 2], pack2(e0, e1));
+        lsum[h / 2 + 1] = add2(lsum[h / 2 + 1], pack2(e2, e3));
+        split_p(e0, e1, e2, e3, ph[h / 4], pl[h / 4]);
       }
       // PV of the tile before has read P^T, and O^T holds its sum
       if (i > 0) {
-        const bool got = mbar_wait(bar(B_PVDONE), (i - 1) & 1, abort_flag, p.status, p.wait_ns);
+        const bool got = wait_phase(bar(B_PVDONE), (i - 1) & 1, abort_flag, p.status, p.wait_ns);
         fail = __any_sync(0xffffffffu, fail || !got);
         tc_fence_after();
       }
-      if (resc && !first) {
+      if (rescale_o) {
 #pragma unroll 1
         for (int mb = 0; mb < 4 && !fail; ++mb) {
           const uint32_t ta = tmem + 64u * mb + hcol + lane_off;
           uint32_t x[HPW];
-          DSA_TMEM_LD_X32(ta, x);
+          DSA_TMEM_LD_X16(ta, x);
 #pragma unroll
           for (int c = 0; c < HPW; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * alpha[hcol + c]);
-          DSA_TMEM_ST_X32(ta, x);
+          DSA_TMEM_ST_X16(ta, x);
         }
       }
-#pragma unroll
-      for (int c = 0; c < HPW / 16; ++c) {
-        const uint32_t off = sw64_off(key, (hcol >> 4) + c);
-        *reinterpret_cast<uint4*>(smem + OFF_P + off) = make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
-        *reinterpret_cast<uint4*>(smem + OFF_P + RSUB + off) = make_uint4(pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
-      }
+      const uint32_t off = sw64_off(key, hh);
+      *reinterpret_cast<uint4*>(smem + OFF_P + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+      *reinterpret_cast<uint4*>(smem + OFF_P + RSUB + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -518,57 +719,73 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
       {
-        const bool got = mbar_wait(bar(B_PVDONE), i & 1, abort_flag, p.status, p.wait_ns);
+        const bool got = wait_phase(bar(B_PVDONE), i & 1, abort_flag, p.status, p.wait_ns);
         fail = __any_sync(0xffffffffu, fail || !got);
         tc_fence_after();
       }
-      red[quad * 64 + hcol + lane] = mla::warp_reduce32<false>(lsum, lane);
-      if (named_bar_or(1, SM_THREADS, fail)) {
-        ok = false;
-        break;
+      {
+        float v[HPW];
+#pragma unroll
+        for (int h = 0; h < HPW / 2; ++h) {
+          const float2 w = unpack2(lsum[h]);
+          v[2 * h] = w.x, v[2 * h + 1] = w.y;
+        }
+        const float sum = mla::warp_reduce16<false>(v, lane);
+        if ((lane & 1) == 0) red[quad * 64 + hcol + lane / 2] = sum;
       }
+      if (named_bar_or(1 + hh, 128, fail)) break;
       float l = 0.f;  // row sum of head hcol + lane (quadrant 0)
-      if (quad == 0) {
+      const bool owns = quad == 0 && lane < HPW;
+      if (owns) {
         const int h = hcol + lane;
         l = red[h] + red[64 + h] + red[128 + h] + red[192 + h];
         alpha[h] = l == 0.f ? 0.f : 1.f / l;
       }
-      named_bar(1, SM_THREADS);
+      named_bar(1 + hh, 128);
       const int32_t row0 = row * tpr;  // this row's first global tile
       if (row0 >= g_begin && row0 + tpr <= g_end) {
         uint16_t* orow = p.out + static_cast<int64_t>(row) * 64 * 512;
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
           uint32_t x[HPW];
-          DSA_TMEM_LD_X32(tmem + 64u * mb + hcol + lane_off, x);
+          DSA_TMEM_LD_X16(tmem + 64u * mb + hcol + lane_off, x);
 #pragma unroll
-          for (int c = 0; c < HPW; ++c) {
-            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(x[c]) * alpha[hcol + c]);
-            orow[(hcol + c) * 512 + mb * 128 + key] = *reinterpret_cast<const uint16_t*>(&o);
+          for (int c = 0; c < HPW; c += 4) {  // 4 heads of one dim per lane -> 4 dims of one head per lane
+            const float4 a = *reinterpret_cast<const float4*>(alpha + hcol + c);
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(__uint_as_float(x[c]) * a.x, __uint_as_float(x[c + 1]) * a.y);
+            const __nv_bfloat162 b1 = __floats2bfloat162_rn(__uint_as_float(x[c + 2]) * a.z, __uint_as_float(x[c + 3]) * a.w);
+            uint32_t u = *reinterpret_cast<const uint32_t*>(&b0), v = *reinterpret_cast<const uint32_t*>(&b1);
+            const uint32_t un = __shfl_xor_sync(0xffffffffu, u, 1), vn = __shfl_xor_sync(0xffffffffu, v, 1);
+            u = lane & 1 ? __byte_perm(un, u, 0x7632) : __byte_perm(u, un, 0x5410);  // two dims of head c + lane % 2
+            v = lane & 1 ? __byte_perm(vn, v, 0x7632) : __byte_perm(v, vn, 0x5410);  // and of head c + 2 + lane % 2
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u : v, 2);
+            const uint2 w = lane & 2 ? make_uint2(got, v) : make_uint2(u, got);
+            *reinterpret_cast<uint2*>(orow + (hcol + c + (lane & 3)) * 512 + mb * 128 + (key & ~3)) = w;
           }
         }
-        if (p.lse && quad == 0)
+        if (p.lse && owns)
           p.lse[static_cast<int64_t>(row) * 64 + hcol + lane] =
-              l == 0.f ? -INFINITY : (m_run[hcol + lane] - BIAS + log2f(l)) * 0.69314718055994531f;
+              l == 0.f ? -INFINITY : (log2f(l) - nm[hcol + lane]) * 0.69314718055994531f;
       } else {
         const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
-        float* po = p.part_o + pr * 64 * 512;
+        float4* po = reinterpret_cast<float4*>(p.part_o + pr * 64 * 512);  // [16 head quads][512 dims] of 4 heads
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
           uint32_t x[HPW];
-          DSA_TMEM_LD_X32(tmem + 64u * mb + hcol + lane_off, x);
+          DSA_TMEM_LD_X16(tmem + 64u * mb + hcol + lane_off, x);
 #pragma unroll
-          for (int c = 0; c < HPW; ++c) po[(hcol + c) * 512 + mb * 128 + key] = __uint_as_float(x[c]);
+          for (int c = 0; c < HPW; c += 4)
+            po[((hcol + c) >> 2) * 512 + mb * 128 + key] =
+                make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]), __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
         }
-        if (quad == 0) {
-          p.part_ml[pr * 128 + hcol + lane] = l == 0.f ? -INFINITY : m_run[hcol + lane] - BIAS;
+        if (owns) {
+          p.part_ml[pr * 128 + hcol + lane] = l == 0.f ? -INFINITY : -nm[hcol + lane];
           p.part_ml[pr * 128 + 64 + hcol + lane] = l;
         }
       }
       tc_fence_before();
-      named_bar(1, SM_THREADS);  // m_run, alpha and red are the next item's
+      named_bar(1 + hh, 128);  // nm, alpha and red are the next item's
     }
-    (void)ok;
   }
   tc_fence_before();
   __syncthreads();
@@ -576,59 +793,89 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One CTA per (range
-// boundary, 4 heads), 4 dims per thread; the first boundary inside a row does the row.  A row has at most 16 fragments
-// (k <= 2,048); batches of 8 are loaded before any weight is known, so a row costs one or two memory latencies.
-constexpr int COMBINE_THREADS = 512;
+// Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block per (4 heads,
+// 128 dims) of a cut row, one dim of 4 heads per thread.  A row has at most 16 fragments (k <= 2,048); one warp forms
+// their weights while the fragments, 8 at a time, are on their way to everyone: one or two memory latencies.
+// blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first inside a row does it).
+constexpr int COMBINE_THREADS = 128;
 __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* __restrict__ part_o,
                                                                    const float* __restrict__ part_ml, int32_t tpr,
-                                                                   int32_t tiles, int32_t grid,
+                                                                   int32_t quot, int32_t rem, int32_t grid, int32_t by_row,
                                                                    uint16_t* __restrict__ out, float* __restrict__ lse) {
   grid_dependency_sync();
-  const int32_t c = blockIdx.x + 1, h = blockIdx.y * 4 + threadIdx.x / 128, t = threadIdx.x % 128;
-  const int32_t b = range_begin(c, tiles, grid), row = b / tpr;
-  if (b % tpr == 0 || range_begin(c - 1, tiles, grid) > row * tpr) return;
-  int32_t n = 2;  // fragments: CTA c - 1 (its fragment 1), then CTAs c, c + 1, ... (their fragment 0)
-  while (c + n - 1 < grid && range_begin(c + n - 1, tiles, grid) < (row + 1) * tpr) ++n;
-  auto at = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? 1 : 0); };
+  __shared__ float wgt[16][4], inv[4];
+  const int32_t hq = blockIdx.y, dim = blockIdx.z * COMBINE_THREADS + threadIdx.x;
+  int32_t row, c;  // the row's first fragment is CTA c - 1's
+  if (by_row) {
+    row = blockIdx.x;
+    // the first boundary past the row's first tile
+    c = row * tpr * grid / (quot * grid + rem);
+    while (c < grid && range_begin(c, quot, rem, grid) <= row * tpr) ++c;
+    if (c >= grid || range_begin(c, quot, rem, grid) >= (row + 1) * tpr) return;
+  } else {
+    c = blockIdx.x + 1;
+    const int32_t b = range_begin(c, quot, rem, grid);
+    row = b / tpr;
+    if (b % tpr == 0 || range_begin(c - 1, quot, rem, grid) > row * tpr) return;
+  }
+  int32_t n = 2;  // CTA c - 1 (its fragment 1), then CTAs c, c + 1, ... (their fragment 0)
+  while (c + n - 1 < grid && range_begin(c + n - 1, quot, rem, grid) < (row + 1) * tpr) ++n;
+  auto frag = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? 1 : 0); };
   constexpr int EARLY = 8;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float M = -INFINITY, L = 0.f;
-  for (int s0 = 0; s0 < n; s0 += EARLY) {
-    float4 o[EARLY];
-    float m[EARLY], l[EARLY];
+  float4 o[EARLY];
+  auto fetch = [&](int s0) {
 #pragma unroll
-    for (int u = 0; u < EARLY; ++u) {
-      const bool in = s0 + u < n;
-      const int64_t f = at(s0 + u);
-      o[u] = in ? *reinterpret_cast<const float4*>(part_o + (f * 64 + h) * 512 + 4 * t) : make_float4(0.f, 0.f, 0.f, 0.f);
-      m[u] = in ? part_ml[f * 128 + h] : -INFINITY;
-      l[u] = in ? part_ml[f * 128 + 64 + h] : 0.f;
+    for (int u = 0; u < EARLY; ++u)
+      o[u] = s0 + u < n ? reinterpret_cast<const float4*>(part_o)[(frag(s0 + u) * 16 + hq) * 512 + dim]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(0);
+  if (threadIdx.x < 32) {  // lane = (fragment, head) of fragments 0..7, and the same of 8..15
+    const int s = threadIdx.x >> 2, e = threadIdx.x & 3;
+    float m[2], l[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool in = s + 8 * u < n;
+      m[u] = in ? part_ml[frag(s + 8 * u) * 128 + hq * 4 + e] : -INFINITY;
+      l[u] = in ? part_ml[frag(s + 8 * u) * 128 + 64 + hq * 4 + e] : 0.f;
     }
-    float mn = M;
+    float M = fmaxf(m[0], m[1]);
 #pragma unroll
-    for (int u = 0; u < EARLY; ++u) mn = fmaxf(mn, m[u]);
-    const float a = M == -INFINITY ? 0.f : exp2f(M - mn);
-    acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a, L *= a;
+    for (int d = 4; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float L = 0.f;
 #pragma unroll
-    for (int u = 0; u < EARLY; ++u) {
-      if (l[u] == 0.f) continue;  // a fragment without a key
-      const float w = exp2f(m[u] - (mn == -INFINITY ? 0.f : mn));
-      acc.x = fmaf(w, o[u].x, acc.x);
-      acc.y = fmaf(w, o[u].y, acc.y);
-      acc.z = fmaf(w, o[u].z, acc.z);
-      acc.w = fmaf(w, o[u].w, acc.w);
+    for (int u = 0; u < 2; ++u) {
+      const float w = l[u] == 0.f ? 0.f : exp2f(m[u] - (M == -INFINITY ? 0.f : M));  // 0: a fragment without a key
+      wgt[s + 8 * u][e] = w;
       L = fmaf(w, l[u], L);
     }
-    M = mn;
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    if (s == 0) {
+      inv[e] = L == 0.f ? 0.f : 1.f / L;
+      if (lse && blockIdx.z == 0)
+        lse[static_cast<int64_t>(row) * 64 + hq * 4 + e] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 pk;
-  pk.x = *reinterpret_cast<const uint32_t*>(&x);
-  pk.y = *reinterpret_cast<const uint32_t*>(&y);
-  *reinterpret_cast<uint2*>(out + (static_cast<int64_t>(row) * 64 + h) * 512 + 4 * t) = pk;
-  if (lse && t == 0) lse[static_cast<int64_t>(row) * 64 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += EARLY) {
+    if (s0 > 0) fetch(s0);
+#pragma unroll
+    for (int u = 0; u < EARLY; ++u) {
+      const float4 w = *reinterpret_cast<const float4*>(wgt[s0 + u]);
+      acc.x = fmaf(w.x, o[u].x, acc.x);
+      acc.y = fmaf(w.y, o[u].y, acc.y);
+      acc.z = fmaf(w.z, o[u].z, acc.z);
+      acc.w = fmaf(w.w, o[u].w, acc.w);
+    }
+  }
+  const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat16 v = __float2bfloat16_rn(a[e] * inv[e]);
+    out[(static_cast<int64_t>(row) * 64 + hq * 4 + e) * 512 + dim] = *reinterpret_cast<const uint16_t*>(&v);
+  }
 }
 
 }  // namespace mla4

@@ -247,6 +247,24 @@ __host__ __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {
                :                                                                                              \
                : "memory")
 
+// The same for two loads of 16 columns.
+#define DSA_TMEM_LD_X16_NOWAIT(taddr, r)                                                                      \
+  asm volatile(                                                                                               \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),       \
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])  \
+      : "r"(taddr)                                                                                            \
+      : "memory")
+#define DSA_TMEM_WAIT_LD_X16(a, b)                                                                            \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                               \
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]),          \
+                 "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]),      \
+                 "+r"(a[14]), "+r"(a[15]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]),        \
+                 "+r"(b[5]), "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]),        \
+                 "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])                                           \
+               :                                                                                              \
+               : "memory")
+
 // No instruction: orders a second load's registers after a preceding DSA_TMEM_WAIT_LD (which
 // waits for all of the thread's outstanding TMEM loads), so the compiler reads them no earlier.
 #define DSA_TMEM_TIE(r)                                                                                       \

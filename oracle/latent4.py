@@ -21,8 +21,9 @@ def decode_rows(rows):
         mag = MAGS[(w >> (4 * i)) & 7]
         sign = (w >> (8 * i + 7 if i < 4 else 8 * (i - 4) + 3)) & 1
         e = rows[:, 288 + d // 32].astype(np.int64)
-        scale = np.where(e == 255, np.nan, 2.0 ** (np.clip(e, 114, 140) - 127.0))
-        out[:, d] = np.where(sign == 1, -mag, mag) * scale
+        v = np.where(sign == 1, -mag, mag) * 2.0 ** (e - 127.0)
+        # at exponent 14 code 7 is NaN (and every other code, like every other exponent, has no meaning)
+        out[:, d] = np.where((e >= 114) & (e <= 140), v, np.nan)
     return out
 
 
@@ -44,7 +45,9 @@ def encode_rows(y):
         for b in range(18):
             blk = y[r, 32 * b:32 * b + 32]
             if np.isnan(blk).any():
-                out[r, 288 + b] = 255
+                out[r, 288 + b] = 141
+                for w in range(4 * b, 4 * b + 4):
+                    words[w] = 0x77777777
                 continue
             e = block_exponent(blk)
             out[r, 288 + b] = e + 127

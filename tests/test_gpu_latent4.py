@@ -52,7 +52,9 @@ def paged(rng, lens, extra=2):
 
 def garbage_pool(n_pages):
     """A pool whose every row is NaN until it is written: a row read without being selected shows."""
-    return np.full((n_pages, 64, 320), 255, dtype=np.uint8)
+    pool = np.full((n_pages, 64, 320), 141, dtype=np.uint8)
+    pool[:, :, :288] = 0x77
+    return pool
 
 
 def make_rows(rng, n, spread=1.0):
@@ -450,7 +452,8 @@ def test_attention_passes_nan_on_to_its_heads_only():
     t_in, t_out = int(idx[0, 11]), int(np.setdiff1d(np.arange(300), idx[0])[0])
     pool, _, bt, _ = view._keep
     for t, spoiled in ((t_out, False), (t_in, True)):
-        pool.view(-1, 320)[int(bt[0, t // 64]) * 64 + t % 64, 288:306] = 255
+        row = pool.view(-1, 320)[int(bt[0, t // 64]) * 64 + t % 64]
+        row[:288], row[288:306] = 0x77, 141
         out, _ = dsa.sparse_mla_attn(torch.nan_to_num(qd, 0, 0, 0), view, i32_dev(idx), 200, SCALE, rows)
         assert bool(torch.isnan(out).all()) == spoiled and bool(torch.isnan(out).any()) == spoiled
 

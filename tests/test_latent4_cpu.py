@@ -28,7 +28,7 @@ def test_row_format_hand_values():
     row[0, 288] = 129
     v = L4.decode_rows(row)[0]
     assert v[0] == 24.0 and v[1] == -2.0 and v[7] == -16.0 and np.all(v[2:7] == 0) and np.all(v[8:] == 0)
-    row[0, 288] = 255
+    row[0, 288], row[0, 0:16] = 141, 0x77
     assert np.isnan(L4.decode_rows(row)[0, :32]).all()
 
 
@@ -40,9 +40,11 @@ def test_encoder_rounds_to_the_nearest_value_and_decodes_back():
     y[2, 16:32] = 0
     y[3, 32] = 1e6      # saturates at 6 * 2^13
     y[3, 64] = np.inf
+    y[4, 70] = np.nan
     v = L4.decode_rows(L4.encode_rows(y))
     assert list(v[2, :16]) == [0, 1, 1, 2, 2, 4, 4, 6, 0, -1, -1, -2, -2, -4, -4, -6]
     assert v[3, 32] == 49152 and v[3, 64] == 49152 and np.all(v[1, :32] == 0)
+    assert np.isnan(v[4, 64:96]).all() and np.isnan(v).sum() == 32
     for b in range(18):
         blk, got = y[0, 32 * b:32 * b + 32].astype(np.float64), v[0, 32 * b:32 * b + 32]
         step = 2.0 ** L4.block_exponent(blk)
