@@ -35,14 +35,14 @@ namespace mla4 {
 constexpr int TILE = 128;
 constexpr int SUB = 128 * 128;  // one sub-tile: 128 keys (or q parts) x 128 dims, 1 byte each
 constexpr int RSUB = 128 * 64;  // the RoPE dims of 128 keys (or q parts)
-constexpr int SLOTS = 8;
+constexpr int SLOTS = 8;  // sub-tiles; filled and freed in pairs ("halves" of a tile)
 constexpr int OFF_Q = 0;
 constexpr int OFF_QR = 4 * SUB;
 constexpr int OFF_KV = OFF_QR + RSUB;
 constexpr int OFF_KR = OFF_KV + SLOTS * SUB;
 constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][128 keys][64 heads]
 constexpr int OFF_MISC = OFF_P + 2 * RSUB;
-constexpr int N_BARS = 6 + SLOTS * 2 + 1;
+constexpr int N_BARS = 5 + SLOTS;
 constexpr int M_TMEM = 208, M_ABORT = 212;
 constexpr int M_NEED = 192;  // uint8 [4 head groups][4 tiles]: "a head's maximum moved"
 constexpr int M_MASK = 224;  // uint16 [4 tiles][8 warps]: keys that count
@@ -65,8 +65,7 @@ constexpr int REGS_LAUNCH = 72, REGS_SM = 64, REGS_DEC = 96, REGS_MMA = 56;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256;  // S^T buffers at columns 256 and 384; O^T at 0..255
 
-constexpr int B_QFULL = 0, B_SFULL = 1 /* and 2 */, B_PFULL = 3, B_PVDONE = 4, B_RFULL = 5, B_FULL = 6,
-              B_EMPTY = B_FULL + SLOTS;
+constexpr int B_QFULL = 0, B_SFULL = 1 /* and 2 */, B_PFULL = 3, B_PVDONE = 4, B_FULL = 5, B_EMPTY = B_FULL + SLOTS / 2;
 
 // p is held as 2^(z + nm), nm = BIAS - m: at most 2^(BIAS + GROW) <= 256 (e4m3 ends at 448) while the running maximum m
 // trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
@@ -269,8 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     mbar_init(bar(B_SFULL + 1), 2);
     mbar_init(bar(B_PFULL), SM_WARPS);
     mbar_init(bar(B_PVDONE), 1);
-    mbar_init(bar(B_RFULL), DEC_WARPS);
-    for (int i = 0; i < SLOTS; ++i) {
+    for (int i = 0; i < SLOTS / 2; ++i) {
       mbar_init(bar(B_FULL + i), DEC_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
     }
@@ -377,25 +375,37 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
     };
-    // selected position of key 16 dw + lane of tile i (lanes 0..15), -1 past the end
-    auto load_idx = [&](int32_t i) -> int32_t {
-      const int32_t row = (g_begin + i) / tpr, at = (g_begin + i) % tpr * TILE + 16 * dw + lane;
-      return load_if(i < n && lane < 16 && at < p.k, p.idx + static_cast<int64_t>(row / p.rows_per_idx) * p.k + at);
-    };
-    // Its cache slot, in two steps a tile apart, so that no step waits for the load of the one before: the page number
-    // of a position, then the slot (a position or page out of range is reported and skipped).
+    // The cache slot of key 16 dw + lane (lanes 0..15) of a tile, in three steps a tile apart, so that no step waits for
+    // the load of the one before: the selected position (-1: none), its page number, the slot.  `ahead` walks the tiles.
+    // A position or page out of range is reported and skipped.
     struct Pos {
-      int32_t t, len;  // selected position of key 16 dw + lane (-1: none), the sequence's length
+      int32_t t, len, irow;
     };
     struct Page {
       int32_t t, page;
     };
-    auto position = [&](int32_t i) -> Pos {
-      return Pos{load_idx(i), load_if(i < n, p.seq_lens + (g_begin + i) / tpr / p.rows_per_idx)};
+    struct {
+      int32_t left, at, row, irow;
+    } ahead;
+    ahead.left = n;
+    ahead.row = g_begin / tpr;
+    ahead.irow = ahead.row / p.rows_per_idx;
+    ahead.at = g_begin % tpr * TILE + 16 * dw + lane;
+    auto position = [&]() -> Pos {
+      const bool in = ahead.left > 0;
+      const Pos q{load_if(in && lane < 16 && ahead.at < p.k, p.idx + static_cast<int64_t>(ahead.irow) * p.k + ahead.at),
+                  load_if(in, p.seq_lens + ahead.irow), ahead.irow};
+      --ahead.left;
+      ahead.at += TILE;
+      if (ahead.at >= tpr * TILE) {
+        ahead.at = 16 * dw + lane;
+        ahead.irow = ++ahead.row / p.rows_per_idx;
+      }
+      return q;
     };
-    auto find_page = [&](int32_t i, const Pos& q) -> Page {
-      const int64_t at = static_cast<int64_t>((g_begin + i) / tpr / p.rows_per_idx) * p.max_pages + (q.t >> 6);
-      return Page{q.t, load_if(q.t >= 0 && q.t < q.len && (q.t >> 6) < p.max_pages, p.block_table + at)};
+    auto find_page = [&](const Pos& q) -> Page {
+      return Page{q.t, load_if(q.t >= 0 && q.t < q.len && (q.t >> 6) < p.max_pages,
+                               p.block_table + static_cast<int64_t>(q.irow) * p.max_pages + (q.t >> 6))};
     };
     auto find_slot = [&](const Page& g) -> int32_t {
       if (g.t < 0) return -1;
@@ -431,56 +441,68 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     };
     bool ok = true;
     if (n > 0) q_copy(g_begin / tpr, warp, Q_WARPS);
-    const Pos t0 = position(0), t1 = position(1), t2 = position(2);
-    Pos t3 = position(3);  // in the loop: of tile i + 3
-    const Page g0 = find_page(0, t0), g1 = find_page(1, t1);
-    Page g2 = find_page(2, t2);  // of tile i + 2
+    const Pos t0 = position(), t1 = position(), t2 = position();
+    Pos t3 = position();  // in the loop: of tile i + 3
+    const Page g0 = find_page(t0), g1 = find_page(t1);
+    Page g2 = find_page(t2);  // of tile i + 2
     int32_t slot = find_slot(g0), slot_next;
     load(slot);
     slot_next = find_slot(g1);
-    int32_t item = 0;
+    int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
     if (n > 0) q_split(0, warp, Q_WARPS);
+    const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
     for (int32_t i = 0; i < n && ok; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
-      const uint32_t xa[4] = {ex_a.x, ex_a.y, ex_a.z, ex_a.w}, xb[4] = {ex_b.x, ex_b.y, ex_b.z, ex_b.w};
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int s = 4 * (i & 1) + d;
-        if (ok && i >= 2) ok = wait(B_EMPTY + s, ((i >> 1) & 1) ^ 1);
-        if (ok) {
-          if (d == 0 && lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
-          uint4 o0, o1;
-          uint8_t* dst = smem + OFF_KV + s * SUB;
-          decode32(raw[2 * d], __byte_perm(xa[d], 0, 0x4440u | c4), o0, o1);
-          *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4, 2 * c4)) = o0;
-          *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4, 2 * c4 + 1)) = o1;
-          decode32(raw[2 * d + 1], __byte_perm(xb[d], 0, 0x4440u | c4), o0, o1);
-          *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4 + 8, 2 * c4)) = o0;
-          *reinterpret_cast<uint4*>(dst + sw128_off(16 * dw + r4 + 8, 2 * c4 + 1)) = o1;
-          publish(B_FULL + s);
+      for (int half = 0; half < 2; ++half) {
+        const int b = 2 * (i & 1) + half;
+        if (i >= 2) ok = wait(B_EMPTY + b, ((i >> 1) & 1) ^ 1);
+        if (!ok) break;
+        if (half == 0) {
+          if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
+        } else {
+          // S^T of the tile before has read its RoPE sub-tile (and, at the start of a row, the last row's queries)
+          if (i >= 1) ok = wait(B_SFULL + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+          if (!ok) break;
         }
+#pragma unroll
+        for (int d = 2 * half; d < 2 * half + 2; ++d) {
+          uint4 o0, o1;
+          uint8_t* dst = smem + OFF_KV + (4 * (i & 1) + d) * SUB;
+          const uint32_t xa = d == 0 ? ex_a.x : d == 1 ? ex_a.y : d == 2 ? ex_a.z : ex_a.w;
+          const uint32_t xb = d == 0 ? ex_b.x : d == 1 ? ex_b.y : d == 2 ? ex_b.z : ex_b.w;
+          decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
+          *reinterpret_cast<uint4*>(dst + sa) = o0;
+          *reinterpret_cast<uint4*>(dst + sb) = o1;
+          decode32(raw[2 * d + 1], __byte_perm(xb, 0, 0x4440u | c4), o0, o1);
+          *reinterpret_cast<uint4*>(dst + sa + 1024) = o0;  // 8 rows further: the same swizzle
+          *reinterpret_cast<uint4*>(dst + sb + 1024) = o1;
+        }
+        if (half == 1) {
+          uint4 o0, o1;
+          decode32(raw_r, ex_r, o0, o1);
+          const uint32_t o = sw64_off(16 * dw + (lane >> 1), 2 * (lane & 1));
+          *reinterpret_cast<uint4*>(smem + OFF_KR + o) = o0;
+          *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
+        }
+        publish(B_FULL + b);
       }
-      // S^T of the tile before has read its RoPE sub-tile (and its query row)
-      if (ok && i >= 1) ok = wait(B_SFULL + ((i - 1) & 1), ((i - 1) >> 1) & 1);
-      if (i + 2 < n && (g_begin + i + 2) % tpr == 0) q_prefetch((g_begin + i + 2) / tpr);
-      if (ok && i >= 1 && (g_begin + i) % tpr == 0) {
-        q_copy((g_begin + i) / tpr, dw, DEC_WARPS);
-        q_split(++item, dw, DEC_WARPS);
-      }
-      if (ok) {
-        uint4 o0, o1;
-        decode32(raw_r, ex_r, o0, o1);
-        uint8_t* dst = smem + OFF_KR;
-        const int r = 16 * dw + (lane >> 1), b = lane & 1;
-        *reinterpret_cast<uint4*>(dst + sw64_off(r, 2 * b)) = o0;
-        *reinterpret_cast<uint4*>(dst + sw64_off(r, 2 * b + 1)) = o1;
-        publish(B_RFULL);
-      }
+      if (!ok) break;
       load(slot_next);
       slot = slot_next;
       slot_next = find_slot(g2);
-      g2 = find_page(i + 3, t3);
-      t3 = position(i + 4);
+      g2 = find_page(t3);
+      t3 = position();
+      // the next tile begins a row: its queries as soon as the last S^T that reads the present ones is through
+      if (row_left == 3 && i + 3 < n) q_prefetch(row + 1);
+      if (--row_left == 0 && i + 1 < n) {
+        row_left = tpr;
+        ++row;
+        ok = wait(B_SFULL + (i & 1), (i >> 1) & 1);
+        if (!ok) break;
+        q_copy(row, dw, DEC_WARPS);
+        q_split(++item, dw, DEC_WARPS);
+      }
     }
   } else if (warp >= MMA_WARP) {
     // ================================================================= MMA issuer
@@ -494,8 +516,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       const uint32_t lo0 = (base >> 4) | (1u << 16);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto ready = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_test(bar(b), par)) != 0; };
-      // Two streams of steps, taken as their inputs become ready: S^T of tile `st` (sub-tile `sd` next; 4 = the RoPE dims)
-      // and PV of tile `pt`.  S^T runs up to two tiles ahead of PV.
+      // Two streams of steps, taken as their inputs become ready: S^T of tile `st` (half `sd` next, the second with the RoPE
+      // dims) and PV of tile `pt`.  S^T runs up to two tiles ahead of PV.
       int32_t st = 0, sd = 0, pt = 0, items = 0, row_left = tpr - g_begin % tpr, pv_left = 0;
       bool q_ready = false, pv_first = true;
       pv_left = row_left;
@@ -505,26 +527,26 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         if (st < n) {
           if (!q_ready) q_ready = ready(B_QFULL, items & 1);
           if (q_ready) {
-            const int s = 4 * (st & 1) + sd;
             const uint32_t ds = tm + TM_S + 128u * (st & 1);
-            if (sd < 4 ? ready(B_FULL + s, (st >> 1) & 1) : ready(B_RFULL, st & 1)) {
+            if (ready(B_FULL + 2 * (st & 1) + sd, (st >> 1) & 1)) {
               tc_fence_after();
-              if (sd < 4) {
-                const uint64_t a = desc128(lo0 + (OFF_KV + s * SUB) / 16), b = desc128(lo0 + (OFF_Q + sd * SUB) / 16);
-                if (elect_one()) {
-                  mma_f8(ds, a, b, ID_S, sd != 0);
+              const uint64_t a = desc128(lo0 + (OFF_KV + (4 * (st & 1) + 2 * sd) * SUB) / 16);
+              const uint64_t b = desc128(lo0 + (OFF_Q + 2 * sd * SUB) / 16);
+              const uint32_t keep = sd;
+              if (elect_one()) {
 #pragma unroll
-                  for (int kk = 1; kk < 4; ++kk) mma_f8(ds, a + 2 * kk, b + 2 * kk, ID_S, 1);
-                }
-                ++sd;
-              } else {
-                const uint64_t a = desc64(lo0 + OFF_KR / 16), b = desc64(lo0 + OFF_QR / 16);
-                if (elect_one()) {
-                  mma_f8(ds, a, b, ID_S, 1);
-                  mma_f8(ds, a + 2, b + 2, ID_S, 1);
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_f8(ds, a + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S,
+                         kk > 0 ? 1u : keep);
+                if (sd == 1) {
+                  const uint64_t ar = desc64(lo0 + OFF_KR / 16), br = desc64(lo0 + OFF_QR / 16);
+                  mma_f8(ds, ar, br, ID_S, 1);
+                  mma_f8(ds, ar + 2, br + 2, ID_S, 1);
                   mma_commit(bar(B_SFULL + (st & 1)));
                   mbar_arrive(bar(B_SFULL + (st & 1)));  // and what the decode warps left in shared memory (masks, scales)
                 }
+              }
+              if (++sd == 2) {
                 sd = 0;
                 ++st;
                 if (--row_left == 0) {
@@ -549,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
                 mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 128 * kk, ID_PV, kk > 0 ? 1u : keep);
                 mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 128 * kk, ID_PVR, 1);
               }
-              mma_commit(bar(B_EMPTY + 4 * (pt & 1) + mb));
+              if (mb & 1) mma_commit(bar(B_EMPTY + 2 * (pt & 1) + (mb >> 1)));
             }
             mma_commit(bar(B_PVDONE));
           }
