@@ -76,7 +76,7 @@ __device__ __forceinline__ uint2 word_to_e5m2(uint32_t w, uint2 tab) {
   const uint32_t m = w & 0x77777777u;
   uint2 r;
   r.x = __byte_perm(tab.x, tab.y, m) | (w & 0x80808080u);
-  r.y = __byte_perm(tab.x, tab.y, m >> 16) | ((w * 16u) & 0x80808080u);
+  r.y = __byte_perm(tab.x, tab.y, __umulhi(m, 65536u)) | ((w * 16u) & 0x80808080u);
   return r;
 }
 

@@ -18,7 +18,7 @@
 // j + 2 is decoded into the sub-tiles it frees.
 //
 // Warps 0..15: softmax and output (warp w: TMEM lane quadrant w % 4, 16 heads from 16 (w / 4)); 8 decode warps: the
-// query rows, and tile g + 1's 320-byte rows loaded into registers while tile g is decoded; last warp: MMA issuer.
+// query rows, and tile g + 1's 320-byte rows loaded into registers while tile g is decoded; 2 warps issue the MMAs.
 // CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a range boundary cuts
 // leave fp32 partials for combine4_kernel.
 #pragma once
@@ -44,13 +44,10 @@ constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][128 keys][64 heads]
 constexpr int OFF_MISC = OFF_P + 2 * RSUB;
 constexpr int N_BARS = 5 + SLOTS;
 constexpr int M_TMEM = 208, M_ABORT = 212;
-constexpr int M_NEED = 192;  // uint8 [4 head groups][4 tiles]: "a head's maximum moved"
 constexpr int M_MASK = 224;  // uint16 [4 tiles][8 warps]: keys that count
 constexpr int M_ZS = 288;    // float [4 items][64]: logit scale of a head
-constexpr int M_NM = M_ZS + 1024;    // float [64]: BIAS minus the running maximum (log2 units) of a head
-constexpr int M_ALPHA = M_NM + 256;  // float [64]: 2 to the power of its change; after an item's last tile: the
-                                     // inverse row sums
-constexpr int M_RED = M_ALPHA + 256; // float [4 quadrants][64]; the first 64 also take the change of nm
+constexpr int M_ALPHA = M_ZS + 1024;  // float [64]: factor on a head's sums; after its last tile: inverse row sum
+constexpr int M_RED = M_ALPHA + 256;  // float [4 quadrants][64]
 constexpr int SMEM_BYTES = OFF_MISC + M_RED + 1024;
 static_assert(N_BARS * 8 <= M_TMEM && SMEM_BYTES <= 232448, "shared memory");
 
@@ -67,9 +64,10 @@ constexpr uint32_t TM_S = 256;  // S^T buffers at columns 256 and 384; O^T at 0.
 
 constexpr int B_QFULL = 0, B_SFULL = 1 /* and 2 */, B_PFULL = 3, B_PVDONE = 4, B_FULL = 5, B_EMPTY = B_FULL + SLOTS / 2;
 
-// p is held as 2^(z + nm), nm = BIAS - m: at most 2^(BIAS + GROW) <= 256 (e4m3 ends at 448) while the running maximum m
-// trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
-constexpr float BIAS = 4.f, GROW = 4.f;
+// p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
+// maximum m trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
+constexpr float BIAS = -4.f, GROW = 4.f;
+static_assert(BIAS + GROW == 0.f, "e <= 1");
 
 struct Params {
   const uint16_t* q;  // [n_q, 64, 576] bf16
@@ -165,19 +163,27 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Four probabilities to e4m3 bytes and e5m2 bytes of the rest.  An e5m2 number is the high byte of an f16: adding half
-// of its last place and taking the high bytes rounds to nearest (ties away from zero), without a conversion.
-__device__ __forceinline__ void split_p(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+// Four values e = p / 256 to the e4m3 bytes and, of the rest, the e5m2 bytes of p.  At this scale the f16 of e has the
+// exponent field of p's e4m3 (bias 15 against 7 + 8), normal or not: rounding it to three mantissa bits and taking its
+// bits 14..7 is the conversion.  An e5m2 number is the high byte of an f16.  Both round to nearest (ties away from zero) by
+// adding half a last place; two ALU operations a pair instead of five conversions and permutations.
+__device__ __forceinline__ void split_p(float a, float b, float c, float d, uint32_t one, uint32_t& hi, uint32_t& lo) {
   const __half2 u = __floats2half2_rn(a, b), v = __floats2half2_rn(c, d);
-  const __half2_raw ur = u, vr = v;
-  const uint32_t hu = __nv_cvt_halfraw2_to_fp8x2(ur, __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hv = __nv_cvt_halfraw2_to_fp8x2(vr, __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw bu = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hu), __NV_E4M3);
-  const __half2_raw bv = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hv), __NV_E4M3);
-  const __half2 ru = __hsub2(u, __half2(bu)), rv = __hsub2(v, __half2(bv));
-  hi = __byte_perm(hu, hv, 0x5410);
-  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&ru) + 0x00800080u,
-                   *reinterpret_cast<const uint32_t*>(&rv) + 0x00800080u, 0x7531);
+  // multiply-adds by an opaque 1 (the FMA pipe; the ALU is the busier one)
+  const uint32_t ru = *reinterpret_cast<const uint32_t*>(&u) * one + 0x00400040u;
+  const uint32_t rv = *reinterpret_cast<const uint32_t*>(&v) * one + 0x00400040u;
+  hi = __byte_perm(ru * 2u, rv * 2u, 0x7531);
+  const uint32_t tu = ru & 0xFF80FF80u, tv = rv & 0xFF80FF80u;
+  const __half2 scale = __float2half2_rn(256.f);
+  const __half2 su = __hmul2(__hsub2(u, *reinterpret_cast<const __half2*>(&tu)), scale);
+  const __half2 sv = __hmul2(__hsub2(v, *reinterpret_cast<const __half2*>(&tv)), scale);
+  lo = __byte_perm(*reinterpret_cast<const uint32_t*>(&su) * one + 0x00800080u,
+                   *reinterpret_cast<const uint32_t*>(&sv) * one + 0x00800080u, 0x7531);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // *ptr where `cond` holds, else -1 (and no access).  Nothing waits for the load before its result is used, as it would
@@ -215,15 +221,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   }
   return true;
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // never sleeps
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -241,6 +238,13 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Four 8x8 matrices of 16-bit elements (fragment order) to the 16-byte rows that the lanes address.
+__device__ __forceinline__ void store_matrix(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+
 __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_constant__ Params p) {
   grid_dependency_sync();
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -250,13 +254,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   auto bar = [&](int i) { return bar0 + 8u * i; };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + M_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + M_ABORT);
-  volatile uint8_t* need_flags = misc + M_NEED;
   volatile uint16_t* masks = reinterpret_cast<volatile uint16_t*>(misc + M_MASK);
   float* zs = reinterpret_cast<float*>(misc + M_ZS);
-  float* nm = reinterpret_cast<float*>(misc + M_NM);
   float* alpha = reinterpret_cast<float*>(misc + M_ALPHA);
   float* red = reinterpret_cast<float*>(misc + M_RED);
-  float* delta = red;  // written by the one thread that has read the head's four maxima
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: a uniform value
   if (base & 1023u) {  // the swizzled layouts need it; the driver places dynamic shared memory so
     if (threadIdx.x == 0) atomicOr(p.status, DEVERR_TIMEOUT);
@@ -273,7 +274,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       mbar_init(bar(B_EMPTY + i), 1);
     }
     *abort_flag = 0;
-    for (int i = 0; i < 16; ++i) need_flags[i] = 0;
     fence_mbar_init();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_holder), 512);
@@ -286,17 +286,21 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   const int32_t g_end = range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
   const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
 
+  // Column of S^T (row of the shared q) of a head: within each 16, the order in which a fragment gives a lane the heads
+  // 4 c .. 4 c + 3.
+  auto q_col = [](int h) { return (h & ~15) + 8 * ((h >> 1) & 1) + 2 * ((h >> 2) & 3) + (h & 1); };
   // A query row: copied as bf16 into the rows that its two parts will fill, then split in place.  A warp takes heads
   // h0, h0 + step, ... two at a time, for their latencies.
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   auto q_copy = [&](int32_t row, int h0, int step) {
     const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152;
     for (int h = h0; h < 64; h += step) {
+      const int col = q_col(h);
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         const int c = lane + 32 * u;
-        if (c < 64) cp_async16(base + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7), src + h * 1152 + c * 16, 16);
-        else if (c < 72) cp_async16(base + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3), src + h * 1152 + c * 16, 16);
+        if (c < 64) cp_async16(base + OFF_Q + (c >> 4) * SUB + sw128_off(col + 64 * ((c >> 3) & 1), c & 7), src + h * 1152 + c * 16, 16);
+        else if (c < 72) cp_async16(base + OFF_QR + sw64_off(col + 64 * ((c >> 2) & 1), c & 3), src + h * 1152 + c * 16, 16);
       }
     }
   };
@@ -309,14 +313,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       uint32_t amax[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int h = min(h1 + e * step, 63);
+        const int col = q_col(min(h1 + e * step, 63));
         uint32_t am = 0;
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const int c = lane + 32 * u;
           uint4 x = zero;
-          if (c < 64) x = *reinterpret_cast<const uint4*>(smem + OFF_Q + (c >> 4) * SUB + sw128_off(h + 64 * ((c >> 3) & 1), c & 7));
-          else if (c < 72) x = *reinterpret_cast<const uint4*>(smem + OFF_QR + sw64_off(h + 64 * ((c >> 2) & 1), c & 3));
+          if (c < 64) x = *reinterpret_cast<const uint4*>(smem + OFF_Q + (c >> 4) * SUB + sw128_off(col + 64 * ((c >> 3) & 1), c & 7));
+          else if (c < 72) x = *reinterpret_cast<const uint4*>(smem + OFF_QR + sw64_off(col + 64 * ((c >> 2) & 1), c & 3));
           am = max_u16x2(max_u16x2(am, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
           am = max_u16x2(max_u16x2(am, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
           v[e][u] = x;
@@ -332,6 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       for (int e = 0; e < 2; ++e) {
         const int h = h1 + e * step;
         if (h >= 64) break;
+        const int col = q_col(h);
         const uint32_t am = max(amax[e] & 0xFFFFu, amax[e] >> 16);  // bf16 bits of the largest magnitude
         const bool nan = am >= 0x7F80u;  // a head that is not finite becomes NaN throughout
         int sh = am == 0u || nan ? 0 : 134 - static_cast<int>(am >> 7);
@@ -344,12 +349,12 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           split_q(v[e][u], mul, hi, lo);
           if (c < 64) {
             uint8_t* d = smem + OFF_Q + (c >> 4) * SUB + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d + sw128_off(h, (c & 15) >> 1)) = hi;
-            *reinterpret_cast<uint2*>(d + sw128_off(64 + h, (c & 15) >> 1)) = lo;
+            *reinterpret_cast<uint2*>(d + sw128_off(col, (c & 15) >> 1)) = hi;
+            *reinterpret_cast<uint2*>(d + sw128_off(64 + col, (c & 15) >> 1)) = lo;
           } else if (c < 72) {
             uint8_t* d = smem + OFF_QR + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d + sw64_off(h, (c & 7) >> 1)) = hi;
-            *reinterpret_cast<uint2*>(d + sw64_off(64 + h, (c & 7) >> 1)) = lo;
+            *reinterpret_cast<uint2*>(d + sw64_off(col, (c & 7) >> 1)) = hi;
+            *reinterpret_cast<uint2*>(d + sw64_off(64 + col, (c & 7) >> 1)) = lo;
           }
         }
         if (lane == 0) zs[(item & 3) * 64 + h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
@@ -415,7 +420,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       }
       return g.page * 64 + (g.t & 63);
     };
-    uint4 raw[8], raw_r, ex_a, ex_b;
+    uint4 raw[8], raw_r;
+    uint2 ex_a[2], ex_b[2];
     uint32_t ex_r;
     auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {
       const int32_t s = __shfl_sync(0xffffffffu, slot, src);
@@ -423,16 +429,23 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     };
     auto ld16 = [&](const uint8_t* r, int off) { return r ? __ldg(reinterpret_cast<const uint4*>(r + off)) : zero; };
 
-    auto load = [&](int32_t slots) {
-      const uint8_t *a = row_ptr(slots, r4), *b = row_ptr(slots, r4 + 8), *c = row_ptr(slots, lane >> 1);
-      ex_a = ld16(a, lat::EXP_OFF), ex_b = ld16(b, lat::EXP_OFF);
+    const uint8_t *ra, *rb, *rr;  // rows of this lane's blocks
+    auto rows_of = [&](int32_t slots) {
+      ra = row_ptr(slots, r4), rb = row_ptr(slots, r4 + 8), rr = row_ptr(slots, lane >> 1);
+    };
+    auto load_half = [&](int half) {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        raw[2 * d] = ld16(a, d * 64 + c4 * 16);
-        raw[2 * d + 1] = ld16(b, d * 64 + c4 * 16);
+      for (int d = 2 * half; d < 2 * half + 2; ++d) {
+        raw[2 * d] = ld16(ra, d * 64 + c4 * 16);
+        raw[2 * d + 1] = ld16(rb, d * 64 + c4 * 16);
       }
-      raw_r = ld16(c, 256 + (lane & 1) * 16);
-      ex_r = c ? __ldg(c + lat::EXP_OFF + 16 + (lane & 1)) : 0u;
+      const uint2 none = make_uint2(0u, 0u);
+      ex_a[half] = ra ? __ldg(reinterpret_cast<const uint2*>(ra + lat::EXP_OFF + 8 * half)) : none;
+      ex_b[half] = rb ? __ldg(reinterpret_cast<const uint2*>(rb + lat::EXP_OFF + 8 * half)) : none;
+      if (half == 1) {
+        raw_r = ld16(rr, 256 + (lane & 1) * 16);
+        ex_r = rr ? __ldg(rr + lat::EXP_OFF + 16 + (lane & 1)) : 0u;
+      }
     };
 
     auto q_prefetch = [&](int32_t row) {  // 72 lines of this warp's heads
@@ -446,13 +459,16 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     const Page g0 = find_page(t0), g1 = find_page(t1);
     Page g2 = find_page(t2);  // of tile i + 2
     int32_t slot = find_slot(g0), slot_next;
-    load(slot);
+    rows_of(slot);
+    load_half(0);
+    load_half(1);
     slot_next = find_slot(g1);
     int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
     if (n > 0) q_split(0, warp, Q_WARPS);
     const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
     for (int32_t i = 0; i < n && ok; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
+      rows_of(slot_next);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int b = 2 * (i & 1) + half;
@@ -469,8 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         for (int d = 2 * half; d < 2 * half + 2; ++d) {
           uint4 o0, o1;
           uint8_t* dst = smem + OFF_KV + (4 * (i & 1) + d) * SUB;
-          const uint32_t xa = d == 0 ? ex_a.x : d == 1 ? ex_a.y : d == 2 ? ex_a.z : ex_a.w;
-          const uint32_t xb = d == 0 ? ex_b.x : d == 1 ? ex_b.y : d == 2 ? ex_b.z : ex_b.w;
+          const uint32_t xa = d & 1 ? ex_a[half].y : ex_a[half].x, xb = d & 1 ? ex_b[half].y : ex_b[half].x;
           decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
           *reinterpret_cast<uint4*>(dst + sa) = o0;
           *reinterpret_cast<uint4*>(dst + sb) = o1;
@@ -486,9 +501,9 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
         }
         publish(B_FULL + b);
+        load_half(half);  // of the next tile
       }
       if (!ok) break;
-      load(slot_next);
       slot = slot_next;
       slot_next = find_slot(g2);
       g2 = find_page(t3);
@@ -507,93 +522,73 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   } else if (warp >= MMA_WARP) {
     // ================================================================= MMA issuer
     regs_dec<REGS_MMA>();
+    // Two warps, so that neither product waits behind the other's inputs: S^T of a tile as its halves are decoded, PV as
+    // its probabilities arrive (S^T runs up to two tiles ahead).  A whole warp runs each loop and one elected lane issues:
+    // every address stays in uniform registers, and an MMA costs one instruction.  (Issued by one lane of a divergent branch
+    // they took 75 to 120 clocks each; one warp that polled for both streams left the tensor core idle between steps.)
+    const uint32_t lo0 = (base >> 4) | (1u << 16);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait = [&](int b, uint32_t par) {
+      const bool got = __all_sync(0xffffffffu, wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns));
+      tc_fence_after();
+      return got;
+    };
     if (warp == MMA_WARP) {
-      // The whole warp runs the loop, and one elected lane issues: every address stays in uniform registers, and an MMA
-      // costs one instruction.  (Issued by one lane of a divergent branch they took 75 to 120 clocks each.)
-      constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);   // e5m2 keys, e4m3 q parts
+      constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);  // e5m2 keys, e4m3 q parts
+      int32_t row_left = 0, item = 0;
+      bool ok = true;
+      for (int32_t i = 0; i < n && ok; ++i) {
+        if (row_left == 0) {
+          ok = wait(B_QFULL, item++ & 1);
+          row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+        }
+        --row_left;
+        const uint32_t ds = tm + TM_S + 128u * (i & 1);
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = wait(B_FULL + 2 * (i & 1) + half, (i >> 1) & 1);
+          const uint64_t a = desc128(lo0 + (OFF_KV + (4 * (i & 1) + 2 * half) * SUB) / 16);
+          const uint64_t b = desc128(lo0 + (OFF_Q + 2 * half * SUB) / 16);
+          const uint32_t keep = half;
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_f8(ds, a + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S,
+                     kk > 0 ? 1u : keep);
+            if (half == 1) {
+              const uint64_t ar = desc64(lo0 + OFF_KR / 16), br = desc64(lo0 + OFF_QR / 16);
+              mma_f8(ds, ar, br, ID_S, 1);
+              mma_f8(ds, ar + 2, br + 2, ID_S, 1);
+              mma_commit(bar(B_SFULL + (i & 1)));
+              mbar_arrive(bar(B_SFULL + (i & 1)));  // and what the decode warps left in shared memory (masks, scales)
+            }
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == MMA_WARP + 1) {
       constexpr uint32_t ID_PV = make_idesc(1, 0, 1, 1, 128, 64);   // e5m2 values, e4m3 p
       constexpr uint32_t ID_PVR = make_idesc(1, 1, 1, 1, 128, 64);  // and the e5m2 rest of p
-      const uint32_t lo0 = (base >> 4) | (1u << 16);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      auto ready = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, mbar_test(bar(b), par)) != 0; };
-      // Two streams of steps, taken as their inputs become ready: S^T of tile `st` (half `sd` next, the second with the RoPE
-      // dims) and PV of tile `pt`.  S^T runs up to two tiles ahead of PV.
-      int32_t st = 0, sd = 0, pt = 0, items = 0, row_left = tpr - g_begin % tpr, pv_left = 0;
-      bool q_ready = false, pv_first = true;
-      pv_left = row_left;
-      uint64_t since = 0;
-      while (pt < n) {
-        bool moved = false;
-        if (st < n) {
-          if (!q_ready) q_ready = ready(B_QFULL, items & 1);
-          if (q_ready) {
-            const uint32_t ds = tm + TM_S + 128u * (st & 1);
-            if (ready(B_FULL + 2 * (st & 1) + sd, (st >> 1) & 1)) {
-              tc_fence_after();
-              const uint64_t a = desc128(lo0 + (OFF_KV + (4 * (st & 1) + 2 * sd) * SUB) / 16);
-              const uint64_t b = desc128(lo0 + (OFF_Q + 2 * sd * SUB) / 16);
-              const uint32_t keep = sd;
-              if (elect_one()) {
+      int32_t row_left = 0;
+      for (int32_t i = 0; i < n; ++i) {
+        const uint32_t keep = row_left == 0 ? 0u : 1u;  // a row's first tile starts its sum
+        if (row_left == 0) row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+        --row_left;
+        if (!wait(B_PFULL, i & 1)) break;
+        const uint64_t a = desc128(lo0 + (OFF_KV + 4 * (i & 1) * SUB) / 16), b = desc64(lo0 + OFF_P / 16);
+        if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  mma_f8(ds, a + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S,
-                         kk > 0 ? 1u : keep);
-                if (sd == 1) {
-                  const uint64_t ar = desc64(lo0 + OFF_KR / 16), br = desc64(lo0 + OFF_QR / 16);
-                  mma_f8(ds, ar, br, ID_S, 1);
-                  mma_f8(ds, ar + 2, br + 2, ID_S, 1);
-                  mma_commit(bar(B_SFULL + (st & 1)));
-                  mbar_arrive(bar(B_SFULL + (st & 1)));  // and what the decode warps left in shared memory (masks, scales)
-                }
-              }
-              if (++sd == 2) {
-                sd = 0;
-                ++st;
-                if (--row_left == 0) {
-                  row_left = tpr;
-                  q_ready = false;
-                  ++items;
-                }
-              }
-              moved = true;
+          for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {  // 32 keys: 4 groups of 8 rows
+              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 128 * kk, ID_PV, kk > 0 ? 1u : keep);
+              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 128 * kk, ID_PVR, 1);
             }
+            if (mb & 1) mma_commit(bar(B_EMPTY + 2 * (i & 1) + (mb >> 1)));
           }
-        }
-        if (pt < st && ready(B_PFULL, pt & 1)) {
-          tc_fence_after();
-          const uint64_t a = desc128(lo0 + (OFF_KV + 4 * (pt & 1) * SUB) / 16), b = desc64(lo0 + OFF_P / 16);
-          const uint32_t keep = pv_first ? 0u : 1u;
-          if (elect_one()) {
-#pragma unroll
-            for (int mb = 0; mb < 4; ++mb) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {  // 32 keys: 4 groups of 8 rows
-                mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 128 * kk, ID_PV, kk > 0 ? 1u : keep);
-                mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 128 * kk, ID_PVR, 1);
-              }
-              if (mb & 1) mma_commit(bar(B_EMPTY + 2 * (pt & 1) + (mb >> 1)));
-            }
-            mma_commit(bar(B_PVDONE));
-          }
-          ++pt;
-          pv_first = --pv_left == 0;
-          if (pv_first) pv_left = tpr;
-          moved = true;
+          mma_commit(bar(B_PVDONE));
         }
         __syncwarp();
-        if (moved) {
-          since = 0;
-        } else {  // nothing to issue: bounded like every other wait
-          bool stop = *abort_flag != 0;
-          const uint64_t now = globaltimer_ns();
-          if (since == 0) since = now;
-          if (now - since > p.wait_ns) {
-            *abort_flag = 1;
-            if (lane == 0) atomicOr(p.status, DEVERR_TIMEOUT);
-            stop = true;
-          }
-          if (__any_sync(0xffffffffu, stop)) break;
-        }
       }
     }
   } else {
@@ -603,115 +598,124 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       q_copy(g_begin / tpr, warp, Q_WARPS);
       q_split(0, warp, Q_WARPS);
     }
-    const int quad = warp & 3, hh = warp >> 2;
-    const int key = quad * 32 + lane;  // TMEM lane: key of S^T, dim of an O^T block
+    // The scores come in 16x256b fragments: lane l = 4 r + c holds keys r, r + 8, r + 16, r + 24 of its quadrant for heads
+    // 4 c .. 4 c + 3 of the group, so their scales, maxima and sums stay in registers (with a key per lane they would be 16
+    // heads', read again from shared memory for every tile while the tensor core takes its bandwidth).
+    const int quad = warp & 3, hh = warp >> 2, hcol = HPW * hh;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const int hcol = HPW * hh;
+    const int key = quad * 32 + lane;         // row of P^T this lane addresses; dim of an O^T block
+    const int my = hcol + 4 * (lane & 3);     // first of this lane's four heads
+    uint32_t one;
+    asm volatile("mov.b32 %0, 1;" : "=r"(one));
     int32_t item = 0;
-    uint64_t lsum[HPW / 2];
-    bool seen = false;  // the item has had a key that counts (its maxima are set)
-    // As in mla.cuh: a failed wait is recorded and acted on at the next named_bar_or, where all softmax threads leave
-    // together; before a warp-collective TMEM access the lanes of a warp agree on it.
+    uint64_t zz[2], nn[2], lsum[2];  // scale, BIAS minus the running maximum, row sum; heads (0, 1) and (2, 3)
+    bool seen = false;               // the item has had a key that counts (its maxima are set)
+    // As in mla.cuh: a failed wait is recorded and acted on at the next named_bar_or, where the four warps of a group leave
+    // together (the others by the abort flag); before a warp-collective TMEM access the lanes of a warp agree on it.
     bool fail = false;
+    int32_t row = g_begin / tpr, j = g_begin % tpr;
     for (int32_t i = 0; i < n; ++i) {
-      const int32_t row = (g_begin + i) / tpr, j = (g_begin + i) % tpr;
-      const bool first = i == 0 || j == 0, last = i == n - 1 || j == tpr - 1;
-      if (first) {
-        if (quad == 0 && lane < HPW) nm[hcol + lane] = BIAS;
-        named_bar(1 + hh, 128);
-#pragma unroll
-        for (int h = 0; h < HPW / 2; ++h) lsum[h] = 0ull;
-        seen = false;
-      }
+      const bool last = i == n - 1 || j == tpr - 1;
       {
         const bool got = wait_phase(bar(B_SFULL + (i & 1)), (i >> 1) & 1, abort_flag, p.status, p.wait_ns);
         fail = __any_sync(0xffffffffu, fail || !got);
       }
       tc_fence_after();
-      const uint4 live = *reinterpret_cast<const uint4*>(misc + M_MASK + (i & 3) * 16);
-      const uint32_t mine = quad == 0 ? live.x : quad == 1 ? live.y : quad == 2 ? live.z : live.w;
-      const bool valid = (mine >> lane) & 1;
-      uint64_t t[HPW / 2];  // log2 of p: s * zs + nm, two heads each
-      float top = -INFINITY;
+      if (i == 0 || j == 0) {
+        const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(zs + (item & 3) * 64 + my);
+        zz[0] = z.x, zz[1] = z.y;
+        nn[0] = nn[1] = pack2(BIAS, BIAS);
+        lsum[0] = lsum[1] = 0ull;
+        seen = false;
+      }
+      const uint32_t mine = *reinterpret_cast<const uint32_t*>(misc + M_MASK + (i & 3) * 16 + quad * 4);
+      uint64_t t[8];  // log2 of p, [key r + 8 m][head pair]: t[2 m + pair] = s * zz + nn
       if (!fail) {
-        const float* zi = zs + (item & 3) * 64 + hcol;
         const uint32_t ts = tmem + TM_S + 128u * (i & 1) + hcol + lane_off;
-        const uint64_t part = pack2(0.0625f, 0.0625f);
-        uint32_t a[HPW], b[HPW];
-        DSA_TMEM_LD_X16_NOWAIT(ts, a);
-        DSA_TMEM_LD_X16_NOWAIT(ts + 64u, b);
+        uint32_t a[16], b[16];
+        DSA_TMEM_LD_16X256_X2(ts, a, 0);
+        DSA_TMEM_LD_16X256_X2(ts + (16u << 16), a, 8);
+        DSA_TMEM_LD_16X256_X2(ts + 64u, b, 0);
+        DSA_TMEM_LD_16X256_X2(ts + 64u + (16u << 16), b, 8);
         DSA_TMEM_WAIT_LD_X16(a, b);
+        const uint64_t part = pack2(0.0625f, 0.0625f);
 #pragma unroll
-        for (int h = 0; h < HPW; h += 4) {
-          const ulonglong2 zz = *reinterpret_cast<const ulonglong2*>(zi + h);
-          const ulonglong2 nn = *reinterpret_cast<const ulonglong2*>(nm + hcol + h);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int e = h + 2 * u;
-            const uint64_t sum = fma2(pack2(__uint_as_float(b[e]), __uint_as_float(b[e + 1])), part,
-                                      pack2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
-            t[e / 2] = fma2(sum, u ? zz.y : zz.x, u ? nn.y : nn.x);
-          }
+        for (int u = 0; u < 16; u += 2) {  // registers 8 h + 4 pair + 2 m' + e of lanes' half h: key r + 16 h + 8 m'
+          const uint64_t sum = fma2(pack2(__uint_as_float(b[u]), __uint_as_float(b[u + 1])), part,
+                                    pack2(__uint_as_float(a[u]), __uint_as_float(a[u + 1])));
+          const int pair = (u >> 2) & 1, m = 2 * (u >> 3) + ((u >> 1) & 1);
+          t[2 * m + pair] = fma2(sum, zz[pair], nn[pair]);
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < HPW / 2; ++h) t[h] = 0ull;
+        for (int u = 0; u < 8; ++u) t[u] = 0ull;
       }
       if (mine != 0xFFFFFFFFu) {  // the same in the whole warp
 #pragma unroll
-        for (int h = 0; h < HPW / 2; ++h) t[h] = valid ? t[h] : pack2(-INFINITY, -INFINITY);
+        for (int m = 0; m < 4; ++m)
+          if (!((mine >> (8 * m + (lane >> 2))) & 1u)) t[2 * m] = t[2 * m + 1] = pack2(-INFINITY, -INFINITY);
       }
+      float top = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < HPW / 2; ++h) {
-        const float2 v = unpack2(t[h]);
-        top = fmaxf(top, fmaxf(v.x, v.y));
+      for (int u = 0; u < 8; ++u) {
+        const float2 v = unpack2(t[u]);
+        top = max3(top, v.x, v.y);
       }
-      volatile uint8_t* need = need_flags + 4 * hh + (i & 3);
-      if (__any_sync(0xffffffffu, top > BIAS + GROW) && lane == 0) *need = 1;
-      if (named_bar_or(1 + hh, 128, fail)) break;
-      // a later tile's flag: its last readers have passed this barrier, its next writers wait for the next one
-      if (quad == 0 && lane == 0) need_flags[4 * hh + ((i + 2) & 3)] = 0;
-      const bool resc = *need != 0 || !seen;
-      if (resc) {
-        float v[HPW];
-#pragma unroll
-        for (int h = 0; h < HPW / 2; ++h) {
-          const float2 w = unpack2(t[h]);
-          v[2 * h] = w.x, v[2 * h + 1] = w.y;
+      bool rescale_o = false;
+      // The group's four warps (all keys of its heads) keep the running maxima unless one has outgrown them
+      if (named_bar_or(1 + hh, 128, top > BIAS + GROW || !seen || fail)) {
+        float4 w;  // the warp's maxima of this lane's heads
+        {
+          const float2 a0 = unpack2(t[0]), a1 = unpack2(t[2]), a2 = unpack2(t[4]), a3 = unpack2(t[6]);
+          const float2 b0 = unpack2(t[1]), b1 = unpack2(t[3]), b2 = unpack2(t[5]), b3 = unpack2(t[7]);
+          w = make_float4(fmaxf(fmaxf(a0.x, a1.x), fmaxf(a2.x, a3.x)), fmaxf(fmaxf(a0.y, a1.y), fmaxf(a2.y, a3.y)),
+                          fmaxf(fmaxf(b0.x, b1.x), fmaxf(b2.x, b3.x)), fmaxf(fmaxf(b0.y, b1.y), fmaxf(b2.y, b3.y)));
         }
-        const float most = mla::warp_reduce16<true>(v, lane);  // head lane / 2
-        if ((lane & 1) == 0) red[quad * 64 + hcol + lane / 2] = most;
-        named_bar(1 + hh, 128);
-        if (quad == 0 && lane < HPW) {
-          const int h = hcol + lane;
-          const float tmax = fmaxf(fmaxf(red[h], red[64 + h]), fmaxf(red[128 + h], red[192 + h]));  // z + nm
-          float d = 0.f;
-          if (tmax > -INFINITY && (!seen || tmax > BIAS + GROW)) d = BIAS - tmax;
-          delta[h] = d;
-          alpha[h] = seen ? ex2_approx(d) : 0.f;
-          nm[h] += d;
-        }
-        named_bar(1 + hh, 128);
 #pragma unroll
-        for (int h = 0; h < HPW; h += 4) {
-          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(delta + hcol + h);
-          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(alpha + hcol + h);
-          t[h / 2] = add2(t[h / 2], d.x);
-          t[h / 2 + 1] = add2(t[h / 2 + 1], d.y);
-          lsum[h / 2] = mul2(lsum[h / 2], a.x);
-          lsum[h / 2 + 1] = mul2(lsum[h / 2 + 1], a.y);
+        for (int o = 4; o < 32; o <<= 1) {
+          w.x = fmaxf(w.x, __shfl_xor_sync(0xffffffffu, w.x, o));
+          w.y = fmaxf(w.y, __shfl_xor_sync(0xffffffffu, w.y, o));
+          w.z = fmaxf(w.z, __shfl_xor_sync(0xffffffffu, w.z, o));
+          w.w = fmaxf(w.w, __shfl_xor_sync(0xffffffffu, w.w, o));
+        }
+        if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
+        if (named_bar_or(1 + hh, 128, fail)) break;
+        const float4 r0 = *reinterpret_cast<const float4*>(red + my), r1 = *reinterpret_cast<const float4*>(red + 64 + my);
+        const float4 r2 = *reinterpret_cast<const float4*>(red + 128 + my), r3 = *reinterpret_cast<const float4*>(red + 192 + my);
+        // the change of nn: a head's maximum becomes BIAS where it is the first or has grown past the margin
+        auto change = [&](float a, float b, float c, float d) {
+          const float m = fmaxf(fmaxf(a, b), fmaxf(c, d));
+          return m > -INFINITY && (!seen || m > BIAS + GROW) ? BIAS - m : 0.f;
+        };
+        const float4 d = make_float4(change(r0.x, r1.x, r2.x, r3.x), change(r0.y, r1.y, r2.y, r3.y),
+                                     change(r0.z, r1.z, r2.z, r3.z), change(r0.w, r1.w, r2.w, r3.w));
+        const uint64_t dd[2] = {pack2(d.x, d.y), pack2(d.z, d.w)};
+        rescale_o = seen;
+        if (seen) {
+          const float4 f = make_float4(ex2_approx(d.x), ex2_approx(d.y), ex2_approx(d.z), ex2_approx(d.w));
+          lsum[0] = mul2(lsum[0], pack2(f.x, f.y));
+          lsum[1] = mul2(lsum[1], pack2(f.z, f.w));
+          if (quad == 0 && lane < 4) *reinterpret_cast<float4*>(alpha + my) = f;
+          named_bar(1 + hh, 128);
+        } else {
+          const uint4 live = *reinterpret_cast<const uint4*>(misc + M_MASK + (i & 3) * 16);
+          seen = (live.x | live.y | live.z | live.w) != 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          nn[u] = add2(nn[u], dd[u]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) t[2 * m + u] = add2(t[2 * m + u], dd[u]);
         }
       }
-      const bool rescale_o = resc && seen;
-      seen = seen || (live.x | live.y | live.z | live.w) != 0u;
-      uint32_t ph[HPW / 4], pl[HPW / 4];
+      uint32_t ph[4], pl[4];
 #pragma unroll
-      for (int h = 0; h < HPW; h += 4) {
-        const float2 u = unpack2(t[h / 2]), w = unpack2(t[h / 2 + 1]);
+      for (int m = 0; m < 4; ++m) {
+        const float2 u = unpack2(t[2 * m]), w = unpack2(t[2 * m + 1]);
         const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(w.x), e3 = ex2_approx(w.y);
-        lsum[h / 2] = add2(lsum[h / 2], pack2(e0, e1));
-        lsum[h / 2 + 1] = add2(lsum[h / 2 + 1], pack2(e2, e3));
-        split_p(e0, e1, e2, e3, ph[h / 4], pl[h / 4]);
+        lsum[0] = add2(lsum[0], pack2(e0, e1));
+        lsum[1] = add2(lsum[1], pack2(e2, e3));
+        split_p(e0, e1, e2, e3, one, ph[m], pl[m]);
       }
       // PV of the tile before has read P^T, and O^T holds its sum
       if (i > 0) {
@@ -730,13 +734,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           DSA_TMEM_ST_X16(ta, x);
         }
       }
-      const uint32_t off = sw64_off(key, hh);
-      *reinterpret_cast<uint4*>(smem + OFF_P + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-      *reinterpret_cast<uint4*>(smem + OFF_P + RSUB + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+      const uint32_t at = base + OFF_P + sw64_off(key, hh);
+      store_matrix(at, ph);
+      store_matrix(at + RSUB, pl);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PFULL));
+      ++j;
       if (!last) continue;
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
@@ -746,26 +751,39 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         tc_fence_after();
       }
       {
-        float v[HPW];
+        const float2 u = unpack2(lsum[0]), v = unpack2(lsum[1]);
+        float4 w = make_float4(u.x, u.y, v.x, v.y);
 #pragma unroll
-        for (int h = 0; h < HPW / 2; ++h) {
-          const float2 w = unpack2(lsum[h]);
-          v[2 * h] = w.x, v[2 * h + 1] = w.y;
+        for (int o = 4; o < 32; o <<= 1) {
+          w.x += __shfl_xor_sync(0xffffffffu, w.x, o);
+          w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
+          w.z += __shfl_xor_sync(0xffffffffu, w.z, o);
+          w.w += __shfl_xor_sync(0xffffffffu, w.w, o);
         }
-        const float sum = mla::warp_reduce16<false>(v, lane);
-        if ((lane & 1) == 0) red[quad * 64 + hcol + lane / 2] = sum;
+        if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
       }
       if (named_bar_or(1 + hh, 128, fail)) break;
-      float l = 0.f;  // row sum of head hcol + lane (quadrant 0)
-      const bool owns = quad == 0 && lane < HPW;
-      if (owns) {
-        const int h = hcol + lane;
-        l = red[h] + red[64 + h] + red[128 + h] + red[192 + h];
-        alpha[h] = l == 0.f ? 0.f : 1.f / l;
-      }
-      named_bar(1 + hh, 128);
       const int32_t row0 = row * tpr;  // this row's first global tile
-      if (row0 >= g_begin && row0 + tpr <= g_end) {
+      const bool whole = row0 >= g_begin && row0 + tpr <= g_end;
+      const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
+      if (quad == 0 && lane < 4) {
+        const float2 m0 = unpack2(nn[0]), m1 = unpack2(nn[1]);
+        const float nm[4] = {m0.x, m0.y, m1.x, m1.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = my + e;
+          const float l = 256.f * (red[h] + red[64 + h] + red[128 + h] + red[192 + h]);  // sum of p
+          alpha[h] = l == 0.f ? 0.f : 1.f / l;
+          if (!whole) {
+            p.part_ml[pr * 128 + h] = l == 0.f ? -INFINITY : -nm[e] - 8.f;
+            p.part_ml[pr * 128 + 64 + h] = l;
+          } else if (p.lse) {
+            p.lse[static_cast<int64_t>(row) * 64 + h] = l == 0.f ? -INFINITY : (log2f(l) - nm[e] - 8.f) * 0.69314718055994531f;
+          }
+        }
+      }
+      if (whole) {
+        named_bar(1 + hh, 128);  // alpha
         uint16_t* orow = p.out + static_cast<int64_t>(row) * 64 * 512;
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
@@ -785,11 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
             *reinterpret_cast<uint2*>(orow + (hcol + c + (lane & 3)) * 512 + mb * 128 + (key & ~3)) = w;
           }
         }
-        if (p.lse && owns)
-          p.lse[static_cast<int64_t>(row) * 64 + hcol + lane] =
-              l == 0.f ? -INFINITY : (log2f(l) - nm[hcol + lane]) * 0.69314718055994531f;
       } else {
-        const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
         float4* po = reinterpret_cast<float4*>(p.part_o + pr * 64 * 512);  // [16 head quads][512 dims] of 4 heads
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
@@ -800,13 +814,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
             po[((hcol + c) >> 2) * 512 + mb * 128 + key] =
                 make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]), __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
         }
-        if (owns) {
-          p.part_ml[pr * 128 + hcol + lane] = l == 0.f ? -INFINITY : -nm[hcol + lane];
-          p.part_ml[pr * 128 + 64 + hcol + lane] = l;
-        }
       }
+      ++row;
+      j = 0;
       tc_fence_before();
-      named_bar(1 + hh, 128);  // nm, alpha and red are the next item's
+      named_bar(1 + hh, 128);  // alpha and red are the next item's
     }
   }
   tc_fence_before();

@@ -247,6 +247,14 @@ __host__ __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {
                :                                                                                              \
                : "memory")
 
+// 16 lanes x 16 columns in fragments (no wait): registers o .. o + 7 of r.  Lane 4 a + c gets rows a (o, o + 1) and a + 8
+// (o + 2, o + 3) of columns 2 c, 2 c + 1, and the same of columns 8 + 2 c, 9 + 2 c (o + 4 ..).
+#define DSA_TMEM_LD_16X256_X2(taddr, r, o)                                                                    \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                      \
+               : "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),  \
+                 "=r"(r[o + 6]), "=r"(r[o + 7])                                                               \
+               : "r"(taddr)                                                                                   \
+               : "memory")
 // The same for two loads of 16 columns.
 #define DSA_TMEM_LD_X16_NOWAIT(taddr, r)                                                                      \
   asm volatile(                                                                                               \
