@@ -196,9 +196,11 @@ __device__ __forceinline__ int32_t load_if(bool cond, const int32_t* ptr) {
   return r;
 }
 
-// mbar_wait (ptx.cuh) for warps that wait often: each try sleeps until the phase completes or 20 us have passed, where a
-// loop of short tries would take issue slots from the warps that work.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+// A whole warp waits for a phase.  Each try sleeps until the phase completes or 20 us have passed (a loop of short tries
+// would take issue slots from the warps that work).  A wait that runs out sets the abort flag and the status word; from then
+// on every wait of the CTA gives up after one try.  Nothing leaves its loop early: all roles run through their steps (on
+// whatever the buffers hold) and end together, so none is left waiting for one that has gone.
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                            uint64_t limit_ns) {
   auto attempt = [&] {
     uint32_t ok;
@@ -209,17 +211,16 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
         : "memory");
     return ok != 0;
   };
-  if (attempt()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!attempt()) {
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      *abort = 1;
-      atomicOr(status, DEVERR_TIMEOUT);
-      return false;
+  if (!attempt()) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!*abort && !attempt()) {
+      if (globaltimer_ns() - t0 > limit_ns) {
+        *abort = 1;
+        atomicOr(status, DEVERR_TIMEOUT);
+      }
     }
   }
-  return true;
+  __syncwarp();
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -237,6 +238,9 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// What keys that do not count read instead of a cache row: codes 0 are zeros whatever the exponents.
+__device__ __align__(16) const uint8_t zero_row[lat::ROW4] = {};
 
 // Four 8x8 matrices of 16-bit elements (fragment order) to the 16-byte rows that the lanes address.
 __device__ __forceinline__ void store_matrix(uint32_t addr, const uint32_t (&v)[4]) {
@@ -271,10 +275,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     mbar_init(bar(B_PVDONE), 1);
     for (int i = 0; i < SLOTS / 2; ++i) {
       mbar_init(bar(B_FULL + i), DEC_WARPS);
-      mbar_init(bar(B_EMPTY + i), 1);
+      mbar_init(bar(B_EMPTY + i), 1 + (i & 1));  // second halves: PV and the next S^T
     }
     *abort_flag = 0;
     fence_mbar_init();
+    mbar_arrive(bar(B_EMPTY + 3));  // tile 1 waits for S^T of tile 0 only
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_holder), 512);
   tc_fence_before();
@@ -284,6 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   const int32_t tpr = p.tiles_per_row;
   const int32_t g_begin = range_begin(blockIdx.x, p.quot, p.rem, gridDim.x);
   const int32_t g_end = range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
+  auto wait = [&](int b, uint32_t par) { wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns); };
   const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
 
   // Column of S^T (row of the shared q) of a head: within each 16, the order in which a fragment gives a lane the heads
@@ -372,9 +378,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     // keys l / 4 and l / 4 + 8 (64 consecutive bytes of a row per four lanes); RoPE: block 16 + l % 2 of key l / 2.
     const int dw = warp - SM_WARPS;
     const int c4 = lane & 3, r4 = lane >> 2;
-    auto wait = [&](int b, uint32_t par) {
-      return __all_sync(0xffffffffu, wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns));
-    };
     auto publish = [&](int b) {  // this warp's stores are visible to the tensor core, then one arrival
       fence_async_smem();
       __syncwarp();
@@ -423,11 +426,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     uint4 raw[8], raw_r;
     uint2 ex_a[2], ex_b[2];
     uint32_t ex_r;
-    auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {
+    auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {  // a key that does not count reads a row of zeros
       const int32_t s = __shfl_sync(0xffffffffu, slot, src);
-      return s < 0 ? nullptr : p.kv + static_cast<int64_t>(s) * lat::ROW4;
+      return s < 0 ? zero_row : p.kv + static_cast<int64_t>(s) * lat::ROW4;
     };
-    auto ld16 = [&](const uint8_t* r, int off) { return r ? __ldg(reinterpret_cast<const uint4*>(r + off)) : zero; };
+    auto ld16 = [&](const uint8_t* r, int off) { return __ldg(reinterpret_cast<const uint4*>(r + off)); };
 
     const uint8_t *ra, *rb, *rr;  // rows of this lane's blocks
     auto rows_of = [&](int32_t slots) {
@@ -439,12 +442,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         raw[2 * d] = ld16(ra, d * 64 + c4 * 16);
         raw[2 * d + 1] = ld16(rb, d * 64 + c4 * 16);
       }
-      const uint2 none = make_uint2(0u, 0u);
-      ex_a[half] = ra ? __ldg(reinterpret_cast<const uint2*>(ra + lat::EXP_OFF + 8 * half)) : none;
-      ex_b[half] = rb ? __ldg(reinterpret_cast<const uint2*>(rb + lat::EXP_OFF + 8 * half)) : none;
+      ex_a[half] = __ldg(reinterpret_cast<const uint2*>(ra + lat::EXP_OFF + 8 * half));
+      ex_b[half] = __ldg(reinterpret_cast<const uint2*>(rb + lat::EXP_OFF + 8 * half));
       if (half == 1) {
         raw_r = ld16(rr, 256 + (lane & 1) * 16);
-        ex_r = rr ? __ldg(rr + lat::EXP_OFF + 16 + (lane & 1)) : 0u;
+        ex_r = __ldg(rr + lat::EXP_OFF + 16 + (lane & 1));
       }
     };
 
@@ -452,7 +454,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152 + dw * 8 * 1152;
       for (int l = lane; l < 72; l += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + l * 128));
     };
-    bool ok = true;
     if (n > 0) q_copy(g_begin / tpr, warp, Q_WARPS);
     const Pos t0 = position(), t1 = position(), t2 = position();
     Pos t3 = position();  // in the loop: of tile i + 3
@@ -466,20 +467,18 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
     if (n > 0) q_split(0, warp, Q_WARPS);
     const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
-    for (int32_t i = 0; i < n && ok; ++i) {
+    for (int32_t i = 0; i < n; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
       rows_of(slot_next);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int b = 2 * (i & 1) + half;
-        if (i >= 2) ok = wait(B_EMPTY + b, ((i >> 1) & 1) ^ 1);
-        if (!ok) break;
+        // free once PV of tile i - 2 has read it; the second half, with the one RoPE sub-tile, also once S^T of tile i - 1 has
         if (half == 0) {
+          if (i >= 2) wait(B_EMPTY + b, ((i >> 1) & 1) ^ 1);
           if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
-        } else {
-          // S^T of the tile before has read its RoPE sub-tile (and, at the start of a row, the last row's queries)
-          if (i >= 1) ok = wait(B_SFULL + ((i - 1) & 1), ((i - 1) >> 1) & 1);
-          if (!ok) break;
+        } else if (i >= 1) {
+          wait(B_EMPTY + b, ((i + 1) >> 1) & 1 ^ 1);
         }
 #pragma unroll
         for (int d = 2 * half; d < 2 * half + 2; ++d) {
@@ -503,7 +502,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         publish(B_FULL + b);
         load_half(half);  // of the next tile
       }
-      if (!ok) break;
       slot = slot_next;
       slot_next = find_slot(g2);
       g2 = find_page(t3);
@@ -513,8 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       if (--row_left == 0 && i + 1 < n) {
         row_left = tpr;
         ++row;
-        ok = wait(B_SFULL + (i & 1), (i >> 1) & 1);
-        if (!ok) break;
+        wait(B_SFULL + (i & 1), (i >> 1) & 1);
         q_copy(row, dw, DEC_WARPS);
         q_split(++item, dw, DEC_WARPS);
       }
@@ -528,29 +525,24 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     // they took 75 to 120 clocks each; one warp that polled for both streams left the tensor core idle between steps.)
     const uint32_t lo0 = (base >> 4) | (1u << 16);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    auto wait = [&](int b, uint32_t par) {
-      const bool got = __all_sync(0xffffffffu, wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns));
-      tc_fence_after();
-      return got;
-    };
     if (warp == MMA_WARP) {
       constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);  // e5m2 keys, e4m3 q parts
       int32_t row_left = 0, item = 0;
-      bool ok = true;
-      for (int32_t i = 0; i < n && ok; ++i) {
+      for (int32_t i = 0; i < n; ++i) {
         if (row_left == 0) {
-          ok = wait(B_QFULL, item++ & 1);
+          wait(B_QFULL, item++ & 1);
           row_left = i == 0 ? tpr - g_begin % tpr : tpr;
         }
         --row_left;
         const uint32_t ds = tm + TM_S + 128u * (i & 1);
 #pragma unroll 1
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = wait(B_FULL + 2 * (i & 1) + half, (i >> 1) & 1);
+        for (int half = 0; half < 2; ++half) {
+          wait(B_FULL + 2 * (i & 1) + half, (i >> 1) & 1);
+          tc_fence_after();
           const uint64_t a = desc128(lo0 + (OFF_KV + (4 * (i & 1) + 2 * half) * SUB) / 16);
           const uint64_t b = desc128(lo0 + (OFF_Q + 2 * half * SUB) / 16);
           const uint32_t keep = half;
-          if (ok && elect_one()) {
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_f8(ds, a + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S,
@@ -560,6 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
               mma_f8(ds, ar, br, ID_S, 1);
               mma_f8(ds, ar + 2, br + 2, ID_S, 1);
               mma_commit(bar(B_SFULL + (i & 1)));
+              mma_commit(bar(B_EMPTY + 2 * ((i + 1) & 1) + 1));
               mbar_arrive(bar(B_SFULL + (i & 1)));  // and what the decode warps left in shared memory (masks, scales)
             }
           }
@@ -574,7 +567,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         const uint32_t keep = row_left == 0 ? 0u : 1u;  // a row's first tile starts its sum
         if (row_left == 0) row_left = i == 0 ? tpr - g_begin % tpr : tpr;
         --row_left;
-        if (!wait(B_PFULL, i & 1)) break;
+        wait(B_PFULL, i & 1);
+        tc_fence_after();
         const uint64_t a = desc128(lo0 + (OFF_KV + 4 * (i & 1) * SUB) / 16), b = desc64(lo0 + OFF_P / 16);
         if (elect_one()) {
 #pragma unroll
@@ -610,16 +604,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     int32_t item = 0;
     uint64_t zz[2], nn[2], lsum[2];  // scale, BIAS minus the running maximum, row sum; heads (0, 1) and (2, 3)
     bool seen = false;               // the item has had a key that counts (its maxima are set)
-    // As in mla.cuh: a failed wait is recorded and acted on at the next named_bar_or, where the four warps of a group leave
-    // together (the others by the abort flag); before a warp-collective TMEM access the lanes of a warp agree on it.
-    bool fail = false;
     int32_t row = g_begin / tpr, j = g_begin % tpr;
     for (int32_t i = 0; i < n; ++i) {
       const bool last = i == n - 1 || j == tpr - 1;
-      {
-        const bool got = wait_phase(bar(B_SFULL + (i & 1)), (i >> 1) & 1, abort_flag, p.status, p.wait_ns);
-        fail = __any_sync(0xffffffffu, fail || !got);
-      }
+      wait(B_SFULL + (i & 1), (i >> 1) & 1);
       tc_fence_after();
       if (i == 0 || j == 0) {
         const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(zs + (item & 3) * 64 + my);
@@ -630,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       }
       const uint32_t mine = *reinterpret_cast<const uint32_t*>(misc + M_MASK + (i & 3) * 16 + quad * 4);
       uint64_t t[8];  // log2 of p, [key r + 8 m][head pair]: t[2 m + pair] = s * zz + nn
-      if (!fail) {
+      {
         const uint32_t ts = tmem + TM_S + 128u * (i & 1) + hcol + lane_off;
         uint32_t a[16], b[16];
         DSA_TMEM_LD_16X256_X2(ts, a, 0);
@@ -646,9 +634,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           const int pair = (u >> 2) & 1, m = 2 * (u >> 3) + ((u >> 1) & 1);
           t[2 * m + pair] = fma2(sum, zz[pair], nn[pair]);
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) t[u] = 0ull;
       }
       if (mine != 0xFFFFFFFFu) {  // the same in the whole warp
 #pragma unroll
@@ -663,7 +648,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       }
       bool rescale_o = false;
       // The group's four warps (all keys of its heads) keep the running maxima unless one has outgrown them
-      if (named_bar_or(1 + hh, 128, top > BIAS + GROW || !seen || fail)) {
+      if (named_bar_or(1 + hh, 128, top > BIAS + GROW || !seen)) {
         float4 w;  // the warp's maxima of this lane's heads
         {
           const float2 a0 = unpack2(t[0]), a1 = unpack2(t[2]), a2 = unpack2(t[4]), a3 = unpack2(t[6]);
@@ -679,7 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           w.w = fmaxf(w.w, __shfl_xor_sync(0xffffffffu, w.w, o));
         }
         if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
-        if (named_bar_or(1 + hh, 128, fail)) break;
+        named_bar(1 + hh, 128);
         const float4 r0 = *reinterpret_cast<const float4*>(red + my), r1 = *reinterpret_cast<const float4*>(red + 64 + my);
         const float4 r2 = *reinterpret_cast<const float4*>(red + 128 + my), r3 = *reinterpret_cast<const float4*>(red + 192 + my);
         // the change of nn: a head's maximum becomes BIAS where it is the first or has grown past the margin
@@ -718,14 +703,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         split_p(e0, e1, e2, e3, one, ph[m], pl[m]);
       }
       // PV of the tile before has read P^T, and O^T holds its sum
-      if (i > 0) {
-        const bool got = wait_phase(bar(B_PVDONE), (i - 1) & 1, abort_flag, p.status, p.wait_ns);
-        fail = __any_sync(0xffffffffu, fail || !got);
-        tc_fence_after();
-      }
+      if (i > 0) wait(B_PVDONE, (i - 1) & 1);
+      tc_fence_after();
       if (rescale_o) {
 #pragma unroll 1
-        for (int mb = 0; mb < 4 && !fail; ++mb) {
+        for (int mb = 0; mb < 4; ++mb) {
           const uint32_t ta = tmem + 64u * mb + hcol + lane_off;
           uint32_t x[HPW];
           DSA_TMEM_LD_X16(ta, x);
@@ -745,11 +727,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       if (!last) continue;
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
-      {
-        const bool got = wait_phase(bar(B_PVDONE), i & 1, abort_flag, p.status, p.wait_ns);
-        fail = __any_sync(0xffffffffu, fail || !got);
-        tc_fence_after();
-      }
+      wait(B_PVDONE, i & 1);
+      tc_fence_after();
       {
         const float2 u = unpack2(lsum[0]), v = unpack2(lsum[1]);
         float4 w = make_float4(u.x, u.y, v.x, v.y);
@@ -762,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         }
         if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
       }
-      if (named_bar_or(1 + hh, 128, fail)) break;
+      named_bar(1 + hh, 128);
       const int32_t row0 = row * tpr;  // this row's first global tile
       const bool whole = row0 >= g_begin && row0 + tpr <= g_end;
       const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
