@@ -5,22 +5,23 @@
 //   * a cache value c * 2^e (e2m1 times a power of two in [2^-13, 2^13]) is an e5m2 number, exactly.  Four of them
 //     decode with one byte permutation (a table of the block's eight magnitudes) and one logical operation;
 //   * q is scaled per head by a power of two to a largest magnitude in [128, 256) and split into the nearest e4m3
-//     number and 16 times the rest, also e4m3: 8 significant bits, all that bf16 has.  The two parts are 128 columns
-//     of one product, summed with the factor 1/16 in the softmax;
+//     number and 16 times the rest, also e4m3: 8 significant bits, all that bf16 has.  The two parts are 128 rows of
+//     one product, summed with the factor 1/16 in the softmax;
 //   * p is split into the nearest e4m3 number and the nearest e5m2 number of the rest (7 to 8 bits, as bf16, and a
 //     floor of 2^-20 of the row's largest probability), two products into the same accumulator.
-// In the form of the FP8 kernel (mla.cuh), every MMA has M = 128:
-//   S^T[key, q part] = KV[key, 0:576] . Q[part, 0:576]   N = 128, K = 32: 18 steps of 64 clocks
-//   O^T[dim, head]  += V^T[dim, key] . P^T[key, head]    N = 64, 4 blocks of 128 dims, 2 parts: 32 steps of 48 clocks
-// so a tile of 128 keys takes the tensor core about 2,700 clocks (operand reads at 128 B a clock set both rates).
-// The decoded tile is 72 KB, half of an f16 one, so nearly two tiles fit in shared memory (eight 128-dim sub-tiles in
-// a ring, one RoPE sub-tile): S^T of tile j + 1 runs while the softmax of tile j does, and PV of tile j while tile
-// j + 2 is decoded into the sub-tiles it frees.
+//   S[q part, key]  = Q[part, 0:576] . KV[key, 0:576]    M = 128, N = 128, K = 32: 18 steps of 64 clocks
+//   O^T[dim, head] += V^T[dim, key] . P[head, key]       M = 128 dims x 4, N = 64, K = 32, 2 parts: 32 steps of 48 clocks
+// so a tile of 128 keys takes the tensor core about 2,700 clocks.
 //
-// Warps 0..15: softmax and output (warp w: TMEM lane quadrant w % 4, 16 heads from 16 (w / 4)); 8 decode warps: the
-// query rows, and tile g + 1's 320-byte rows loaded into registers while tile g is decoded; 2 warps issue the MMAs.
-// CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a range boundary cuts
-// leave fp32 partials for combine4_kernel.
+// What bounds it is the chain of one tile (rows, decode, S, softmax, PV), which is several times that long, so three
+// tiles are in flight: a decoded tile is 64 KB (plus 8 KB of RoPE dims, one buffer), and the query row, which would take
+// that much again, stays in tensor memory as the A operand of S.  It passes through a tile's slot of the ring on its way
+// there.  Tensor memory: O^T in columns 0..255, S in 256..383, Q (512 dims) in 384..511; Q's RoPE dims in shared memory.
+//
+// Warps 0..15: softmax and output (warp w: heads 16 (w % 4) .. + 15, keys 32 (w / 4) .. + 31; a lane holds 16 keys of one
+// head); 8 decode warps: the query rows, and the next tile's 320-byte rows loaded into registers while one is decoded;
+// 2 warps issue the MMAs.  CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a
+// range boundary cuts leave fp32 partials for combine4_kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,19 +36,18 @@ namespace mla4 {
 constexpr int TILE = 128;
 constexpr int SUB = 128 * 128;  // one sub-tile: 128 keys (or q parts) x 128 dims, 1 byte each
 constexpr int RSUB = 128 * 64;  // the RoPE dims of 128 keys (or q parts)
-constexpr int SLOTS = 8;  // sub-tiles; filled and freed in pairs ("halves" of a tile)
-constexpr int OFF_Q = 0;
-constexpr int OFF_QR = 4 * SUB;
+constexpr int SLOTS = 3;        // of 4 sub-tiles; filled and freed in two halves
+constexpr int OFF_QR = 0;       // RoPE dims of the 128 q parts
 constexpr int OFF_KV = OFF_QR + RSUB;
-constexpr int OFF_KR = OFF_KV + SLOTS * SUB;
-constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][128 keys][64 heads]
-constexpr int OFF_MISC = OFF_P + 2 * RSUB;
-constexpr int N_BARS = 5 + SLOTS;
+constexpr int OFF_KR = OFF_KV + SLOTS * 4 * SUB;
+constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][64 heads][128 keys]
+constexpr int OFF_MISC = OFF_P + SUB;
+constexpr int N_BARS = 6 + 4 * SLOTS;
 constexpr int M_TMEM = 208, M_ABORT = 212;
 constexpr int M_MASK = 224;  // uint16 [4 tiles][8 warps]: keys that count
 constexpr int M_ZS = 288;    // float [4 items][64]: logit scale of a head
 constexpr int M_ALPHA = M_ZS + 1024;  // float [64]: factor on a head's sums; after its last tile: inverse row sum
-constexpr int M_RED = M_ALPHA + 256;  // float [4 quadrants][64]
+constexpr int M_RED = M_ALPHA + 256;  // float [4 key groups][64]
 constexpr int SMEM_BYTES = OFF_MISC + M_RED + 1024;
 static_assert(N_BARS * 8 <= M_TMEM && SMEM_BYTES <= 232448, "shared memory");
 
@@ -60,9 +60,10 @@ constexpr int THREADS = (MMA_WARP + 4) * 32;  // seven whole warpgroups (three w
 // Spills would go to L2, since shared memory leaves the L1 cache next to nothing.
 constexpr int REGS_LAUNCH = 72, REGS_SM = 64, REGS_DEC = 96, REGS_MMA = 56;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
-constexpr uint32_t TM_S = 256;  // S^T buffers at columns 256 and 384; O^T at 0..255
+constexpr uint32_t TM_S = 256, TM_Q = 384;
 
-constexpr int B_QFULL = 0, B_SFULL = 1 /* and 2 */, B_PFULL = 3, B_PVDONE = 4, B_FULL = 5, B_EMPTY = B_FULL + SLOTS / 2;
+// S complete (and its shared-memory operands free), S read, P written, PV complete; then halves of the ring's slots
+constexpr int B_SFULL = 0, B_SDONE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_FULL = 6, B_EMPTY = B_FULL + 2 * SLOTS;
 
 // p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
 // maximum m trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
@@ -227,8 +228,17 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
-  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(count) : "memory");
+// D += A B^T with A (K-major, 4 bytes per column) in tensor memory.
+__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 128 rows x 32 bytes of shared memory to 8 columns of tensor memory.
+__device__ __forceinline__ void tmem_copy(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -241,13 +251,6 @@ __device__ __forceinline__ void regs_dec() {
 
 // What keys that do not count read instead of a cache row: codes 0 are zeros whatever the exponents.
 __device__ __align__(16) const uint8_t zero_row[lat::ROW4] = {};
-
-// Four 8x8 matrices of 16-bit elements (fragment order) to the 16-byte rows that the lanes address.
-__device__ __forceinline__ void store_matrix(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
-}
 
 __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_constant__ Params p) {
   grid_dependency_sync();
@@ -268,18 +271,17 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     return;
   }
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_QFULL), Q_WARPS);
     mbar_init(bar(B_SFULL), 2);
-    mbar_init(bar(B_SFULL + 1), 2);
+    mbar_init(bar(B_SDONE), 1);
+    mbar_init(bar(B_SREAD), SM_WARPS);
     mbar_init(bar(B_PFULL), SM_WARPS);
     mbar_init(bar(B_PVDONE), 1);
-    for (int i = 0; i < SLOTS / 2; ++i) {
+    for (int i = 0; i < 2 * SLOTS; ++i) {
       mbar_init(bar(B_FULL + i), DEC_WARPS);
-      mbar_init(bar(B_EMPTY + i), 1 + (i & 1));  // second halves: PV and the next S^T
+      mbar_init(bar(B_EMPTY + i), 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
-    mbar_arrive(bar(B_EMPTY + 3));  // tile 1 waits for S^T of tile 0 only
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_holder), 512);
   tc_fence_before();
@@ -292,25 +294,35 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   auto wait = [&](int b, uint32_t par) { wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns); };
   const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
 
-  // Column of S^T (row of the shared q) of a head: within each 16, the order in which a fragment gives a lane the heads
-  // 4 c .. 4 c + 3.
-  auto q_col = [](int h) { return (h & ~15) + 8 * ((h >> 1) & 1) + 2 * ((h >> 2) & 3) + (h & 1); };
-  // A query row: copied as bf16 into the rows that its two parts will fill, then split in place.  A warp takes heads
-  // h0, h0 + step, ... two at a time, for their latencies.
+  // The ring's slots in the order of their use: a row's query, then its tiles.  On a fresh barrier the wait for the phase
+  // before the first passes.
+  struct Ring {
+    int32_t slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++slot == SLOTS) slot = 0, phase ^= 1;
+    }
+  };
+  // Row of S of a head's first part; its second is 16 rows further, in the same lane quadrant of tensor memory.
+  auto q_row = [](int h) { return 32 * (h >> 4) + (h & 15); };
+  // A query row: copied as bf16 into the rows (of a slot, and of the RoPE buffer) that its two parts will fill, then split
+  // in place.  A warp takes heads h0, h0 + step, ... two at a time, for their latencies.
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto q_copy = [&](int32_t row, int h0, int step) {
+  auto q_at = [&](int32_t slot, int row, int c) {  // raw 16-byte chunk c (0..71) of the head whose first part is `row`
+    return c < 64 ? OFF_KV + (4 * slot + (c >> 4)) * SUB + sw128_off(row + 16 * ((c >> 3) & 1), c & 7)
+                  : OFF_QR + sw64_off(row + 16 * ((c >> 2) & 1), c & 3);
+  };
+  auto q_copy = [&](int32_t row, int32_t slot, int h0, int step) {
     const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152;
     for (int h = h0; h < 64; h += step) {
-      const int col = q_col(h);
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         const int c = lane + 32 * u;
-        if (c < 64) cp_async16(base + OFF_Q + (c >> 4) * SUB + sw128_off(col + 64 * ((c >> 3) & 1), c & 7), src + h * 1152 + c * 16, 16);
-        else if (c < 72) cp_async16(base + OFF_QR + sw64_off(col + 64 * ((c >> 2) & 1), c & 3), src + h * 1152 + c * 16, 16);
+        if (c < 72) cp_async16(base + q_at(slot, q_row(h), c), src + h * 1152 + c * 16, 16);
       }
     }
   };
-  auto q_split = [&](int32_t item, int h0, int step) {
+  auto q_split = [&](int32_t item, int32_t slot, int h0, int step) {
     cp_async_wait_all();
     __syncwarp();
 #pragma unroll 1
@@ -319,14 +331,13 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       uint32_t amax[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int col = q_col(min(h1 + e * step, 63));
+        const int row = q_row(min(h1 + e * step, 63));
         uint32_t am = 0;
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const int c = lane + 32 * u;
           uint4 x = zero;
-          if (c < 64) x = *reinterpret_cast<const uint4*>(smem + OFF_Q + (c >> 4) * SUB + sw128_off(col + 64 * ((c >> 3) & 1), c & 7));
-          else if (c < 72) x = *reinterpret_cast<const uint4*>(smem + OFF_QR + sw64_off(col + 64 * ((c >> 2) & 1), c & 3));
+          if (c < 72) x = *reinterpret_cast<const uint4*>(smem + q_at(slot, row, c));
           am = max_u16x2(max_u16x2(am, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
           am = max_u16x2(max_u16x2(am, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
           v[e][u] = x;
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       for (int e = 0; e < 2; ++e) {
         const int h = h1 + e * step;
         if (h >= 64) break;
-        const int col = q_col(h);
+        const int row = q_row(h);
         const uint32_t am = max(amax[e] & 0xFFFFu, amax[e] >> 16);  // bf16 bits of the largest magnitude
         const bool nan = am >= 0x7F80u;  // a head that is not finite becomes NaN throughout
         int sh = am == 0u || nan ? 0 : 134 - static_cast<int>(am >> 7);
@@ -350,17 +361,13 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         const float mul = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
-          const int c = lane + 32 * u;
+          const int c = lane + 32 * u;  // 8 values: 8 bytes of either part
           uint2 hi, lo;
           split_q(v[e][u], mul, hi, lo);
-          if (c < 64) {
-            uint8_t* d = smem + OFF_Q + (c >> 4) * SUB + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d + sw128_off(col, (c & 15) >> 1)) = hi;
-            *reinterpret_cast<uint2*>(d + sw128_off(64 + col, (c & 15) >> 1)) = lo;
-          } else if (c < 72) {
-            uint8_t* d = smem + OFF_QR + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d + sw64_off(col, (c & 7) >> 1)) = hi;
-            *reinterpret_cast<uint2*>(d + sw64_off(64 + col, (c & 7) >> 1)) = lo;
+          if (c < 72) {
+            uint8_t* d = smem + (c < 64 ? OFF_KV + (4 * slot + (c >> 4)) * SUB : OFF_QR) + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(d + (c < 64 ? sw128_off(row, (c & 15) >> 1) : sw64_off(row, (c & 7) >> 1))) = hi;
+            *reinterpret_cast<uint2*>(d + (c < 64 ? sw128_off(row + 16, (c & 15) >> 1) : sw64_off(row + 16, (c & 7) >> 1))) = lo;
           }
         }
         if (lane == 0) zs[(item & 3) * 64 + h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
@@ -368,7 +375,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     }
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_n(bar(B_QFULL), Q_WARPS / step == 1 ? 1 : Q_WARPS / DEC_WARPS);
   };
 
   if (warp >= SM_WARPS && warp < MMA_WARP) {
@@ -454,7 +460,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152 + dw * 8 * 1152;
       for (int l = lane; l < 72; l += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + l * 128));
     };
-    if (n > 0) q_copy(g_begin / tpr, warp, Q_WARPS);
+    Ring ring;
+    if (n > 0) q_copy(g_begin / tpr, 0, warp, Q_WARPS);
     const Pos t0 = position(), t1 = position(), t2 = position();
     Pos t3 = position();  // in the loop: of tile i + 3
     const Page g0 = find_page(t0), g1 = find_page(t1);
@@ -465,25 +472,29 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     load_half(1);
     slot_next = find_slot(g1);
     int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
-    if (n > 0) q_split(0, warp, Q_WARPS);
+    if (n > 0) {
+      q_split(0, 0, warp, Q_WARPS);
+      named_bar(5, Q_WARPS * 32);  // the softmax warps' share of the first query row
+      publish(B_FULL);
+      publish(B_FULL + 1);
+      ring.next();
+    }
     const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
     for (int32_t i = 0; i < n; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
       rows_of(slot_next);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int b = 2 * (i & 1) + half;
-        // free once PV of tile i - 2 has read it; the second half, with the one RoPE sub-tile, also once S^T of tile i - 1 has
+        wait(B_EMPTY + 2 * ring.slot + half, ring.phase ^ 1);
         if (half == 0) {
-          if (i >= 2) wait(B_EMPTY + b, ((i >> 1) & 1) ^ 1);
           if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
         } else if (i >= 1) {
-          wait(B_EMPTY + b, ((i + 1) >> 1) & 1 ^ 1);
+          wait(B_SDONE, (i - 1) & 1);  // the one RoPE sub-tile
         }
 #pragma unroll
         for (int d = 2 * half; d < 2 * half + 2; ++d) {
           uint4 o0, o1;
-          uint8_t* dst = smem + OFF_KV + (4 * (i & 1) + d) * SUB;
+          uint8_t* dst = smem + OFF_KV + (4 * ring.slot + d) * SUB;
           const uint32_t xa = d & 1 ? ex_a[half].y : ex_a[half].x, xb = d & 1 ? ex_b[half].y : ex_b[half].x;
           decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
           *reinterpret_cast<uint4*>(dst + sa) = o0;
@@ -499,21 +510,27 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           *reinterpret_cast<uint4*>(smem + OFF_KR + o) = o0;
           *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
         }
-        publish(B_FULL + b);
+        publish(B_FULL + 2 * ring.slot + half);
         load_half(half);  // of the next tile
       }
+      ring.next();
       slot = slot_next;
       slot_next = find_slot(g2);
       g2 = find_page(t3);
       t3 = position();
-      // the next tile begins a row: its queries as soon as the last S^T that reads the present ones is through
+      // the next tile begins a row: its queries, once S has read the present ones' RoPE dims for the last time
       if (row_left == 3 && i + 3 < n) q_prefetch(row + 1);
       if (--row_left == 0 && i + 1 < n) {
         row_left = tpr;
         ++row;
-        wait(B_SFULL + (i & 1), (i >> 1) & 1);
-        q_copy(row, dw, DEC_WARPS);
-        q_split(++item, dw, DEC_WARPS);
+        wait(B_EMPTY + 2 * ring.slot, ring.phase ^ 1);
+        wait(B_EMPTY + 2 * ring.slot + 1, ring.phase ^ 1);
+        wait(B_SDONE, i & 1);
+        q_copy(row, ring.slot, dw, DEC_WARPS);
+        q_split(++item, ring.slot, dw, DEC_WARPS);
+        publish(B_FULL + 2 * ring.slot);
+        publish(B_FULL + 2 * ring.slot + 1);
+        ring.next();
       }
     }
   } else if (warp >= MMA_WARP) {
@@ -525,120 +542,138 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     // they took 75 to 120 clocks each; one warp that polled for both streams left the tensor core idle between steps.)
     const uint32_t lo0 = (base >> 4) | (1u << 16);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    Ring ring;
+    int32_t row_left = 0;
     if (warp == MMA_WARP) {
-      constexpr uint32_t ID_S = make_idesc(1, 0, 0, 0, 128, 128);  // e5m2 keys, e4m3 q parts
-      int32_t row_left = 0, item = 0;
+      constexpr uint32_t ID_S = make_idesc(0, 1, 0, 0, 128, 128);  // e4m3 q parts, e5m2 keys
       for (int32_t i = 0; i < n; ++i) {
-        if (row_left == 0) {
-          wait(B_QFULL, item++ & 1);
+        if (row_left == 0) {  // the row's query to tensor memory, behind the last S that reads the one before
+          wait(B_FULL + 2 * ring.slot, ring.phase);
+          wait(B_FULL + 2 * ring.slot + 1, ring.phase);
+          if (i > 0) wait(B_SDONE, (i - 1) & 1);
+          tc_fence_after();
+          const uint64_t a = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16);
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) tmem_copy(tm + TM_Q + 8 * c, a + (c >> 2) * (SUB / 16) + 2 * (c & 3));
+            mma_commit(bar(B_EMPTY + 2 * ring.slot));
+            mma_commit(bar(B_EMPTY + 2 * ring.slot + 1));
+          }
+          __syncwarp();
+          ring.next();
           row_left = i == 0 ? tpr - g_begin % tpr : tpr;
         }
         --row_left;
-        const uint32_t ds = tm + TM_S + 128u * (i & 1);
+        if (i > 0) wait(B_SREAD, (i - 1) & 1);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          wait(B_FULL + 2 * (i & 1) + half, (i >> 1) & 1);
+          wait(B_FULL + 2 * ring.slot + half, ring.phase);
           tc_fence_after();
-          const uint64_t a = desc128(lo0 + (OFF_KV + (4 * (i & 1) + 2 * half) * SUB) / 16);
-          const uint64_t b = desc128(lo0 + (OFF_Q + 2 * half * SUB) / 16);
-          const uint32_t keep = half;
+          const uint64_t b = desc128(lo0 + (OFF_KV + (4 * ring.slot + 2 * half) * SUB) / 16);
+          const uint32_t a = tm + TM_Q + 64 * half, keep = half;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_f8(ds, a + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S,
-                     kk > 0 ? 1u : keep);
+              mma_f8_ta(tm + TM_S, a + 8 * kk, b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S, kk > 0 ? 1u : keep);
             if (half == 1) {
-              const uint64_t ar = desc64(lo0 + OFF_KR / 16), br = desc64(lo0 + OFF_QR / 16);
-              mma_f8(ds, ar, br, ID_S, 1);
-              mma_f8(ds, ar + 2, br + 2, ID_S, 1);
-              mma_commit(bar(B_SFULL + (i & 1)));
-              mma_commit(bar(B_EMPTY + 2 * ((i + 1) & 1) + 1));
-              mbar_arrive(bar(B_SFULL + (i & 1)));  // and what the decode warps left in shared memory (masks, scales)
+              const uint64_t ar = desc64(lo0 + OFF_QR / 16), br = desc64(lo0 + OFF_KR / 16);
+              mma_f8(tm + TM_S, ar, br, ID_S, 1);
+              mma_f8(tm + TM_S, ar + 2, br + 2, ID_S, 1);
+              mma_commit(bar(B_SFULL));
+              mma_commit(bar(B_SDONE));
+              mbar_arrive(bar(B_SFULL));  // and what the decode warps left in shared memory (masks, scales)
             }
           }
           __syncwarp();
         }
+        ring.next();
       }
     } else if (warp == MMA_WARP + 1) {
-      constexpr uint32_t ID_PV = make_idesc(1, 0, 1, 1, 128, 64);   // e5m2 values, e4m3 p
-      constexpr uint32_t ID_PVR = make_idesc(1, 1, 1, 1, 128, 64);  // and the e5m2 rest of p
-      int32_t row_left = 0;
+      constexpr uint32_t ID_PV = make_idesc(1, 0, 1, 0, 128, 64);   // e5m2 values, e4m3 p
+      constexpr uint32_t ID_PVR = make_idesc(1, 1, 1, 0, 128, 64);  // and the e5m2 rest of p
       for (int32_t i = 0; i < n; ++i) {
         const uint32_t keep = row_left == 0 ? 0u : 1u;  // a row's first tile starts its sum
-        if (row_left == 0) row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+        if (row_left == 0) {
+          row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+          ring.next();  // past the row's query
+        }
         --row_left;
         wait(B_PFULL, i & 1);
         tc_fence_after();
-        const uint64_t a = desc128(lo0 + (OFF_KV + 4 * (i & 1) * SUB) / 16), b = desc64(lo0 + OFF_P / 16);
+        const uint64_t a = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16), b = desc128(lo0 + OFF_P / 16);
         if (elect_one()) {
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {  // 32 keys: 4 groups of 8 rows
-              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 128 * kk, ID_PV, kk > 0 ? 1u : keep);
-              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 128 * kk, ID_PVR, 1);
+            for (int kk = 0; kk < 4; ++kk) {  // 32 keys: 4 groups of 8 rows of V, 32 bytes of a row of P
+              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 2 * kk, ID_PV, kk > 0 ? 1u : keep);
+              mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 2 * kk, ID_PVR, 1);
             }
-            if (mb & 1) mma_commit(bar(B_EMPTY + 2 * (i & 1) + (mb >> 1)));
+            if (mb & 1) mma_commit(bar(B_EMPTY + 2 * ring.slot + (mb >> 1)));
           }
           mma_commit(bar(B_PVDONE));
         }
         __syncwarp();
+        ring.next();
       }
     }
   } else {
     // ================================================================= softmax / output warps
     regs_dec<REGS_SM>();
     if (n > 0) {
-      q_copy(g_begin / tpr, warp, Q_WARPS);
-      q_split(0, warp, Q_WARPS);
+      q_copy(g_begin / tpr, 0, warp, Q_WARPS);
+      q_split(0, 0, warp, Q_WARPS);
+      asm volatile("bar.arrive 5, %0;" ::"n"(Q_WARPS * 32) : "memory");
     }
-    // The scores come in 16x256b fragments: lane l = 4 r + c holds keys r, r + 8, r + 16, r + 24 of its quadrant for heads
-    // 4 c .. 4 c + 3 of the group, so their scales, maxima and sums stay in registers (with a key per lane they would be 16
-    // heads', read again from shared memory for every tile while the tensor core takes its bandwidth).
-    const int quad = warp & 3, hh = warp >> 2, hcol = HPW * hh;
+    // Lanes l and l + 16 of a warp hold one head's keys 0..15 and 16..31 of the warp's 32: its scale, maximum and sum are one
+    // register each, and a lane's probabilities are 16 consecutive bytes of P.
+    const int quad = warp & 3, grp = warp >> 2;
+    const int head = 16 * quad + (lane & 15), upper = lane >> 4;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const int key = quad * 32 + lane;         // row of P^T this lane addresses; dim of an O^T block
-    const int my = hcol + 4 * (lane & 3);     // first of this lane's four heads
+    const int dim = quad * 32 + lane, hcol = HPW * grp;  // of the O^T fragment this lane scales and writes: 16 heads of a dim
     uint32_t one;
     asm volatile("mov.b32 %0, 1;" : "=r"(one));
     int32_t item = 0;
-    uint64_t zz[2], nn[2], lsum[2];  // scale, BIAS minus the running maximum, row sum; heads (0, 1) and (2, 3)
-    bool seen = false;               // the item has had a key that counts (its maxima are set)
+    float z = 0.f, nn = 0.f;  // logit scale, BIAS minus the running maximum
+    uint64_t lsum = 0ull;     // two partial row sums
+    bool seen = false;        // the item has had a key that counts (its maxima are set)
     int32_t row = g_begin / tpr, j = g_begin % tpr;
     for (int32_t i = 0; i < n; ++i) {
       const bool last = i == n - 1 || j == tpr - 1;
-      wait(B_SFULL + (i & 1), (i >> 1) & 1);
+      wait(B_SFULL, i & 1);
       tc_fence_after();
       if (i == 0 || j == 0) {
-        const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(zs + (item & 3) * 64 + my);
-        zz[0] = z.x, zz[1] = z.y;
-        nn[0] = nn[1] = pack2(BIAS, BIAS);
-        lsum[0] = lsum[1] = 0ull;
+        z = zs[(item & 3) * 64 + head];
+        nn = BIAS;
+        lsum = 0ull;
         seen = false;
       }
-      const uint32_t mine = *reinterpret_cast<const uint32_t*>(misc + M_MASK + (i & 3) * 16 + quad * 4);
-      uint64_t t[8];  // log2 of p, [key r + 8 m][head pair]: t[2 m + pair] = s * zz + nn
+      const uint32_t mine = *reinterpret_cast<const uint32_t*>(misc + M_MASK + (i & 3) * 16 + grp * 4);
+      uint64_t t[8];  // log2 of p / 256 of keys 2 u, 2 u + 1
       {
-        const uint32_t ts = tmem + TM_S + 128u * (i & 1) + hcol + lane_off;
+        const uint32_t ts = tmem + TM_S + 32u * grp + lane_off;
         uint32_t a[16], b[16];
-        DSA_TMEM_LD_16X256_X2(ts, a, 0);
-        DSA_TMEM_LD_16X256_X2(ts + (16u << 16), a, 8);
-        DSA_TMEM_LD_16X256_X2(ts + 64u, b, 0);
-        DSA_TMEM_LD_16X256_X2(ts + 64u + (16u << 16), b, 8);
+        DSA_TMEM_LD_16X32X2_X16(ts, a);
+        DSA_TMEM_LD_16X32X2_X16(ts + (16u << 16), b);
         DSA_TMEM_WAIT_LD_X16(a, b);
-        const uint64_t part = pack2(0.0625f, 0.0625f);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_SREAD));
+        const uint64_t part = pack2(0.0625f, 0.0625f), zz = pack2(z, z), mm = pack2(nn, nn);
 #pragma unroll
-        for (int u = 0; u < 16; u += 2) {  // registers 8 h + 4 pair + 2 m' + e of lanes' half h: key r + 16 h + 8 m'
-          const uint64_t sum = fma2(pack2(__uint_as_float(b[u]), __uint_as_float(b[u + 1])), part,
-                                    pack2(__uint_as_float(a[u]), __uint_as_float(a[u + 1])));
-          const int pair = (u >> 2) & 1, m = 2 * (u >> 3) + ((u >> 1) & 1);
-          t[2 * m + pair] = fma2(sum, zz[pair], nn[pair]);
+        for (int u = 0; u < 8; ++u) {
+          const uint64_t sum = fma2(pack2(__uint_as_float(b[2 * u]), __uint_as_float(b[2 * u + 1])), part,
+                                    pack2(__uint_as_float(a[2 * u]), __uint_as_float(a[2 * u + 1])));
+          t[u] = fma2(sum, zz, mm);
         }
       }
       if (mine != 0xFFFFFFFFu) {  // the same in the whole warp
+        const uint32_t m = mine >> (16 * upper);
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (!((mine >> (8 * m + (lane >> 2))) & 1u)) t[2 * m] = t[2 * m + 1] = pack2(-INFINITY, -INFINITY);
+        for (int u = 0; u < 8; ++u) {
+          const float2 v = unpack2(t[u]);
+          t[u] = pack2((m >> (2 * u)) & 1u ? v.x : -INFINITY, (m >> (2 * u + 1)) & 1u ? v.y : -INFINITY);
+        }
       }
       float top = -INFINITY;
 #pragma unroll
@@ -647,62 +682,37 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         top = max3(top, v.x, v.y);
       }
       bool rescale_o = false;
-      // The group's four warps (all keys of its heads) keep the running maxima unless one has outgrown them
-      if (named_bar_or(1 + hh, 128, top > BIAS + GROW || !seen)) {
-        float4 w;  // the warp's maxima of this lane's heads
-        {
-          const float2 a0 = unpack2(t[0]), a1 = unpack2(t[2]), a2 = unpack2(t[4]), a3 = unpack2(t[6]);
-          const float2 b0 = unpack2(t[1]), b1 = unpack2(t[3]), b2 = unpack2(t[5]), b3 = unpack2(t[7]);
-          w = make_float4(fmaxf(fmaxf(a0.x, a1.x), fmaxf(a2.x, a3.x)), fmaxf(fmaxf(a0.y, a1.y), fmaxf(a2.y, a3.y)),
-                          fmaxf(fmaxf(b0.x, b1.x), fmaxf(b2.x, b3.x)), fmaxf(fmaxf(b0.y, b1.y), fmaxf(b2.y, b3.y)));
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          w.x = fmaxf(w.x, __shfl_xor_sync(0xffffffffu, w.x, o));
-          w.y = fmaxf(w.y, __shfl_xor_sync(0xffffffffu, w.y, o));
-          w.z = fmaxf(w.z, __shfl_xor_sync(0xffffffffu, w.z, o));
-          w.w = fmaxf(w.w, __shfl_xor_sync(0xffffffffu, w.w, o));
-        }
-        if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
-        named_bar(1 + hh, 128);
-        const float4 r0 = *reinterpret_cast<const float4*>(red + my), r1 = *reinterpret_cast<const float4*>(red + 64 + my);
-        const float4 r2 = *reinterpret_cast<const float4*>(red + 128 + my), r3 = *reinterpret_cast<const float4*>(red + 192 + my);
+      // The running maxima stay unless a head has outgrown its own
+      if (named_bar_or(1, SM_THREADS, top > BIAS + GROW || !seen)) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        if (upper == 0) red[grp * 64 + head] = top;
+        named_bar(1, SM_THREADS);
+        const float m = fmaxf(fmaxf(red[head], red[64 + head]), fmaxf(red[128 + head], red[192 + head]));
         // the change of nn: a head's maximum becomes BIAS where it is the first or has grown past the margin
-        auto change = [&](float a, float b, float c, float d) {
-          const float m = fmaxf(fmaxf(a, b), fmaxf(c, d));
-          return m > -INFINITY && (!seen || m > BIAS + GROW) ? BIAS - m : 0.f;
-        };
-        const float4 d = make_float4(change(r0.x, r1.x, r2.x, r3.x), change(r0.y, r1.y, r2.y, r3.y),
-                                     change(r0.z, r1.z, r2.z, r3.z), change(r0.w, r1.w, r2.w, r3.w));
-        const uint64_t dd[2] = {pack2(d.x, d.y), pack2(d.z, d.w)};
+        const float d = m > -INFINITY && (!seen || m > BIAS + GROW) ? BIAS - m : 0.f;
         rescale_o = seen;
         if (seen) {
-          const float4 f = make_float4(ex2_approx(d.x), ex2_approx(d.y), ex2_approx(d.z), ex2_approx(d.w));
-          lsum[0] = mul2(lsum[0], pack2(f.x, f.y));
-          lsum[1] = mul2(lsum[1], pack2(f.z, f.w));
-          if (quad == 0 && lane < 4) *reinterpret_cast<float4*>(alpha + my) = f;
-          named_bar(1 + hh, 128);
+          const float f = ex2_approx(d);
+          lsum = mul2(lsum, pack2(f, f));
+          if (grp == 0 && upper == 0) alpha[head] = f;
+          named_bar(1, SM_THREADS);
         } else {
           const uint4 live = *reinterpret_cast<const uint4*>(misc + M_MASK + (i & 3) * 16);
           seen = (live.x | live.y | live.z | live.w) != 0u;
         }
+        nn += d;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          nn[u] = add2(nn[u], dd[u]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) t[2 * m + u] = add2(t[2 * m + u], dd[u]);
-        }
+        for (int u = 0; u < 8; ++u) t[u] = add2(t[u], pack2(d, d));
       }
       uint32_t ph[4], pl[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 u = unpack2(t[2 * m]), w = unpack2(t[2 * m + 1]);
-        const float e0 = ex2_approx(u.x), e1 = ex2_approx(u.y), e2 = ex2_approx(w.x), e3 = ex2_approx(w.y);
-        lsum[0] = add2(lsum[0], pack2(e0, e1));
-        lsum[1] = add2(lsum[1], pack2(e2, e3));
-        split_p(e0, e1, e2, e3, one, ph[m], pl[m]);
+      for (int u = 0; u < 4; ++u) {
+        const float2 v = unpack2(t[2 * u]), w = unpack2(t[2 * u + 1]);
+        const float e0 = ex2_approx(v.x), e1 = ex2_approx(v.y), e2 = ex2_approx(w.x), e3 = ex2_approx(w.y);
+        lsum = add2(lsum, add2(pack2(e0, e1), pack2(e2, e3)));
+        split_p(e0, e1, e2, e3, one, ph[u], pl[u]);
       }
-      // PV of the tile before has read P^T, and O^T holds its sum
+      // PV of the tile before has read P, and O^T holds its sum
       if (i > 0) wait(B_PVDONE, (i - 1) & 1);
       tc_fence_after();
       if (rescale_o) {
@@ -716,9 +726,9 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           DSA_TMEM_ST_X16(ta, x);
         }
       }
-      const uint32_t at = base + OFF_P + sw64_off(key, hh);
-      store_matrix(at, ph);
-      store_matrix(at + RSUB, pl);
+      uint8_t* const at = smem + OFF_P + sw128_off(head, 2 * grp + upper);
+      *reinterpret_cast<uint4*>(at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+      *reinterpret_cast<uint4*>(at + RSUB) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -727,42 +737,30 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       if (!last) continue;
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
+      {
+        const float2 v = unpack2(lsum);
+        float l = v.x + v.y;
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (upper == 0) red[grp * 64 + head] = l;
+      }
       wait(B_PVDONE, i & 1);
       tc_fence_after();
-      {
-        const float2 u = unpack2(lsum[0]), v = unpack2(lsum[1]);
-        float4 w = make_float4(u.x, u.y, v.x, v.y);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          w.x += __shfl_xor_sync(0xffffffffu, w.x, o);
-          w.y += __shfl_xor_sync(0xffffffffu, w.y, o);
-          w.z += __shfl_xor_sync(0xffffffffu, w.z, o);
-          w.w += __shfl_xor_sync(0xffffffffu, w.w, o);
-        }
-        if (lane < 4) *reinterpret_cast<float4*>(red + quad * 64 + my) = w;
-      }
-      named_bar(1 + hh, 128);
+      named_bar(1, SM_THREADS);
       const int32_t row0 = row * tpr;  // this row's first global tile
       const bool whole = row0 >= g_begin && row0 + tpr <= g_end;
       const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
-      if (quad == 0 && lane < 4) {
-        const float2 m0 = unpack2(nn[0]), m1 = unpack2(nn[1]);
-        const float nm[4] = {m0.x, m0.y, m1.x, m1.y};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = my + e;
-          const float l = 256.f * (red[h] + red[64 + h] + red[128 + h] + red[192 + h]);  // sum of p
-          alpha[h] = l == 0.f ? 0.f : 1.f / l;
-          if (!whole) {
-            p.part_ml[pr * 128 + h] = l == 0.f ? -INFINITY : -nm[e] - 8.f;
-            p.part_ml[pr * 128 + 64 + h] = l;
-          } else if (p.lse) {
-            p.lse[static_cast<int64_t>(row) * 64 + h] = l == 0.f ? -INFINITY : (log2f(l) - nm[e] - 8.f) * 0.69314718055994531f;
-          }
+      if (grp == 0 && upper == 0) {
+        const float l = 256.f * (red[head] + red[64 + head] + red[128 + head] + red[192 + head]);  // sum of p
+        alpha[head] = l == 0.f ? 0.f : 1.f / l;
+        if (!whole) {
+          p.part_ml[pr * 128 + head] = l == 0.f ? -INFINITY : -nn - 8.f;
+          p.part_ml[pr * 128 + 64 + head] = l;
+        } else if (p.lse) {
+          p.lse[static_cast<int64_t>(row) * 64 + head] = l == 0.f ? -INFINITY : (log2f(l) - nn - 8.f) * 0.69314718055994531f;
         }
       }
       if (whole) {
-        named_bar(1 + hh, 128);  // alpha
+        named_bar(1, SM_THREADS);  // alpha
         uint16_t* orow = p.out + static_cast<int64_t>(row) * 64 * 512;
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
@@ -779,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
             v = lane & 1 ? __byte_perm(vn, v, 0x7632) : __byte_perm(v, vn, 0x5410);  // and of head c + 2 + lane % 2
             const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u : v, 2);
             const uint2 w = lane & 2 ? make_uint2(got, v) : make_uint2(u, got);
-            *reinterpret_cast<uint2*>(orow + (hcol + c + (lane & 3)) * 512 + mb * 128 + (key & ~3)) = w;
+            *reinterpret_cast<uint2*>(orow + (hcol + c + (lane & 3)) * 512 + mb * 128 + (dim & ~3)) = w;
           }
         }
       } else {
@@ -790,14 +788,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           DSA_TMEM_LD_X16(tmem + 64u * mb + hcol + lane_off, x);
 #pragma unroll
           for (int c = 0; c < HPW; c += 4)
-            po[((hcol + c) >> 2) * 512 + mb * 128 + key] =
+            po[((hcol + c) >> 2) * 512 + mb * 128 + dim] =
                 make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]), __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
         }
       }
       ++row;
       j = 0;
       tc_fence_before();
-      named_bar(1 + hh, 128);  // alpha and red are the next item's
+      named_bar(1, SM_THREADS);  // alpha and red are the next item's
     }
   }
   tc_fence_before();

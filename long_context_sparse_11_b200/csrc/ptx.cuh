@@ -247,22 +247,15 @@ __host__ __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {
                :                                                                                              \
                : "memory")
 
-// 16 lanes x 16 columns in fragments (no wait): registers o .. o + 7 of r.  Lane 4 a + c gets rows a (o, o + 1) and a + 8
-// (o + 2, o + 3) of columns 2 c, 2 c + 1, and the same of columns 8 + 2 c, 9 + 2 c (o + 4 ..).
-#define DSA_TMEM_LD_16X256_X2(taddr, r, o)                                                                    \
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                      \
-               : "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),  \
-                 "=r"(r[o + 6]), "=r"(r[o + 7])                                                               \
-               : "r"(taddr)                                                                                   \
-               : "memory")
-// The same for two loads of 16 columns.
-#define DSA_TMEM_LD_X16_NOWAIT(taddr, r)                                                                      \
+// 16 lanes x 32 columns (no wait): threads l and l + 16 get columns 0..15 and 16..31 of TMEM lane l.
+#define DSA_TMEM_LD_16X32X2_X16(taddr, r)                                                                     \
   asm volatile(                                                                                               \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" \
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;" \
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),       \
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])  \
       : "r"(taddr)                                                                                            \
       : "memory")
+// Wait for the thread's TMEM loads, two of 16 registers among them.
 #define DSA_TMEM_WAIT_LD_X16(a, b)                                                                            \
   asm volatile("tcgen05.wait::ld.sync.aligned;"                                                               \
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]),          \
