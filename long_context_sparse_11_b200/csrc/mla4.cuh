@@ -53,12 +53,11 @@ static_assert(N_BARS * 8 <= M_TMEM && SMEM_BYTES <= 232448, "shared memory");
 
 constexpr int SM_WARPS = 16, DEC_WARPS = 8, HPW = 16;
 constexpr int SM_THREADS = SM_WARPS * 32;
-constexpr int Q_WARPS = SM_WARPS + DEC_WARPS;  // warps that split the first query row of a CTA (later ones: the decode warps)
 constexpr int MMA_WARP = SM_WARPS + DEC_WARPS;
 constexpr int THREADS = (MMA_WARP + 4) * 32;  // seven whole warpgroups (three warps of the last one idle)
-// Registers per thread: 72 at launch for 896 threads; the softmax and the issuer give some of theirs to the decode.
+// Registers per thread: 72 at launch for 896 threads; the issuers' warpgroup gives some of its own to the decode.
 // Spills would go to L2, since shared memory leaves the L1 cache next to nothing.
-constexpr int REGS_LAUNCH = 72, REGS_SM = 64, REGS_DEC = 96, REGS_MMA = 56;
+constexpr int REGS_LAUNCH = 72, REGS_SM = 72, REGS_DEC = 88, REGS_MMA = 40;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256, TM_Q = 384;
 
@@ -305,76 +304,45 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   };
   // Row of S of a head's first part; its second is 16 rows further, in the same lane quadrant of tensor memory.
   auto q_row = [](int h) { return 32 * (h >> 4) + (h & 15); };
-  // A query row: copied as bf16 into the rows (of a slot, and of the RoPE buffer) that its two parts will fill, then split
-  // in place.  A warp takes heads h0, h0 + step, ... two at a time, for their latencies.
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto q_at = [&](int32_t slot, int row, int c) {  // raw 16-byte chunk c (0..71) of the head whose first part is `row`
-    return c < 64 ? OFF_KV + (4 * slot + (c >> 4)) * SUB + sw128_off(row + 16 * ((c >> 3) & 1), c & 7)
-                  : OFF_QR + sw64_off(row + 16 * ((c >> 2) & 1), c & 3);
-  };
-  auto q_copy = [&](int32_t row, int32_t slot, int h0, int step) {
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q) + static_cast<int64_t>(row) * 64 * 1152;
-    for (int h = h0; h < 64; h += step) {
+  // Four heads of a query row, eight lanes each (lane l % 8 of a head holds 16-byte chunks l % 8 + 8 u; the last are the RoPE
+  // dims), split into the rows of a slot.  The RoPE parts are returned: their one buffer is free only after the last S of
+  // the row before.
+  auto q_stage = [&](int32_t row, int32_t item, int32_t slot, int h4, uint2& rope_hi, uint2& rope_lo) {
+    const int h = h4 + (lane >> 3), l8 = lane & 7, r = q_row(h);
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(row) * 64 + h) * 576) + l8;
+    uint4 v[9];
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const int c = lane + 32 * u;
-        if (c < 72) cp_async16(base + q_at(slot, q_row(h), c), src + h * 1152 + c * 16, 16);
-      }
+    for (int u = 0; u < 9; ++u) v[u] = __ldg(src + 8 * u);
+    uint32_t am = 0;
+#pragma unroll
+    for (int u = 0; u < 9; ++u) {
+      am = max_u16x2(max_u16x2(am, v[u].x & 0x7FFF7FFFu), v[u].y & 0x7FFF7FFFu);
+      am = max_u16x2(max_u16x2(am, v[u].z & 0x7FFF7FFFu), v[u].w & 0x7FFF7FFFu);
     }
-  };
-  auto q_split = [&](int32_t item, int32_t slot, int h0, int step) {
-    cp_async_wait_all();
-    __syncwarp();
-#pragma unroll 1
-    for (int h1 = h0; h1 < 64; h1 += 2 * step) {
-      uint4 v[2][3];
-      uint32_t amax[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = q_row(min(h1 + e * step, 63));
-        uint32_t am = 0;
+    for (int o = 4; o > 0; o >>= 1) am = max_u16x2(am, __shfl_xor_sync(0xffffffffu, am, o));
+    am = max(am & 0xFFFFu, am >> 16);  // bf16 bits of the head's largest magnitude
+    const bool nan = am >= 0x7F80u;    // a head that is not finite becomes NaN throughout
+    int sh = am == 0u || nan ? 0 : 134 - static_cast<int>(am >> 7);
+    sh = min(max(sh, -120), 126);
+    const float mul = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const int c = lane + 32 * u;
-          uint4 x = zero;
-          if (c < 72) x = *reinterpret_cast<const uint4*>(smem + q_at(slot, row, c));
-          am = max_u16x2(max_u16x2(am, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
-          am = max_u16x2(max_u16x2(am, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
-          v[e][u] = x;
-        }
-        amax[e] = am;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) amax[e] = max_u16x2(amax[e], __shfl_xor_sync(0xffffffffu, amax[e], o));
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = h1 + e * step;
-        if (h >= 64) break;
-        const int row = q_row(h);
-        const uint32_t am = max(amax[e] & 0xFFFFu, amax[e] >> 16);  // bf16 bits of the largest magnitude
-        const bool nan = am >= 0x7F80u;  // a head that is not finite becomes NaN throughout
-        int sh = am == 0u || nan ? 0 : 134 - static_cast<int>(am >> 7);
-        sh = min(max(sh, -120), 126);
-        const float mul = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const int c = lane + 32 * u;  // 8 values: 8 bytes of either part
-          uint2 hi, lo;
-          split_q(v[e][u], mul, hi, lo);
-          if (c < 72) {
-            uint8_t* d = smem + (c < 64 ? OFF_KV + (4 * slot + (c >> 4)) * SUB : OFF_QR) + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(d + (c < 64 ? sw128_off(row, (c & 15) >> 1) : sw64_off(row, (c & 7) >> 1))) = hi;
-            *reinterpret_cast<uint2*>(d + (c < 64 ? sw128_off(row + 16, (c & 15) >> 1) : sw64_off(row + 16, (c & 7) >> 1))) = lo;
-          }
-        }
-        if (lane == 0) zs[(item & 3) * 64 + h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-      }
+    for (int u = 0; u < 8; ++u) {  // chunk l8 + 8 u: 8 bytes of either part
+      uint2 hi, lo;
+      split_q(v[u], mul, hi, lo);
+      uint8_t* d = smem + OFF_KV + (4 * slot + (u >> 1)) * SUB + (l8 & 1) * 8;
+      const uint32_t c = 4 * (u & 1) + (l8 >> 1);
+      *reinterpret_cast<uint2*>(d + sw128_off(r, c)) = hi;
+      *reinterpret_cast<uint2*>(d + sw128_off(r + 16, c)) = lo;
     }
-    fence_async_smem();
-    __syncwarp();
+    split_q(v[8], mul, rope_hi, rope_lo);
+    if (l8 == 0) zs[(item & 3) * 64 + h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  };
+  auto q_stage_rope = [&](int h4, const uint2& hi, const uint2& lo) {
+    const int r = q_row(h4 + (lane >> 3)), l8 = lane & 7;
+    uint8_t* d = smem + OFF_QR + (l8 & 1) * 8;
+    *reinterpret_cast<uint2*>(d + sw64_off(r, l8 >> 1)) = hi;
+    *reinterpret_cast<uint2*>(d + sw64_off(r + 16, l8 >> 1)) = lo;
   };
 
   if (warp >= SM_WARPS && warp < MMA_WARP) {
@@ -461,7 +429,6 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       for (int l = lane; l < 72; l += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + l * 128));
     };
     Ring ring;
-    if (n > 0) q_copy(g_begin / tpr, 0, warp, Q_WARPS);
     const Pos t0 = position(), t1 = position(), t2 = position();
     Pos t3 = position();  // in the loop: of tile i + 3
     const Page g0 = find_page(t0), g1 = find_page(t1);
@@ -473,8 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     slot_next = find_slot(g1);
     int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
     if (n > 0) {
-      q_split(0, 0, warp, Q_WARPS);
-      named_bar(5, Q_WARPS * 32);  // the softmax warps' share of the first query row
+      named_bar(2, SM_THREADS + DEC_WARPS * 32);  // the first query row is the softmax warps' work
       publish(B_FULL);
       publish(B_FULL + 1);
       ring.next();
@@ -511,26 +477,32 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
         }
         publish(B_FULL + 2 * ring.slot + half);
-        load_half(half);  // of the next tile
+        if (row_left > 1) load_half(half);  // of the next tile; behind the query where one comes first
       }
       ring.next();
       slot = slot_next;
       slot_next = find_slot(g2);
       g2 = find_page(t3);
       t3 = position();
-      // the next tile begins a row: its queries, once S has read the present ones' RoPE dims for the last time
+      // the next tile begins a row: its queries first
       if (row_left == 3 && i + 3 < n) q_prefetch(row + 1);
       if (--row_left == 0 && i + 1 < n) {
         row_left = tpr;
         ++row;
         wait(B_EMPTY + 2 * ring.slot, ring.phase ^ 1);
         wait(B_EMPTY + 2 * ring.slot + 1, ring.phase ^ 1);
+        uint2 hi[2], lo[2];
+        ++item;
+        q_stage(row, item, ring.slot, 8 * dw, hi[0], lo[0]);
+        q_stage(row, item, ring.slot, 8 * dw + 4, hi[1], lo[1]);
         wait(B_SDONE, i & 1);
-        q_copy(row, ring.slot, dw, DEC_WARPS);
-        q_split(++item, ring.slot, dw, DEC_WARPS);
+        q_stage_rope(8 * dw, hi[0], lo[0]);
+        q_stage_rope(8 * dw + 4, hi[1], lo[1]);
         publish(B_FULL + 2 * ring.slot);
         publish(B_FULL + 2 * ring.slot + 1);
         ring.next();
+        load_half(0);
+        load_half(1);
       }
     }
   } else if (warp >= MMA_WARP) {
@@ -619,11 +591,13 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     }
   } else {
     // ================================================================= softmax / output warps
-    regs_dec<REGS_SM>();
+    static_assert(REGS_SM == REGS_LAUNCH, "no change");
     if (n > 0) {
-      q_copy(g_begin / tpr, 0, warp, Q_WARPS);
-      q_split(0, 0, warp, Q_WARPS);
-      asm volatile("bar.arrive 5, %0;" ::"n"(Q_WARPS * 32) : "memory");
+      uint2 hi, lo;
+      q_stage(g_begin / tpr, 0, 0, 4 * warp, hi, lo);
+      q_stage_rope(4 * warp, hi, lo);
+      fence_async_smem();
+      asm volatile("bar.arrive 2, %0;" ::"n"(SM_THREADS + DEC_WARPS * 32) : "memory");
     }
     // Lanes l and l + 16 of a warp hold one head's keys 0..15 and 16..31 of the warp's 32: its scale, maximum and sum are one
     // register each, and a lane's probabilities are 16 consecutive bytes of P.
