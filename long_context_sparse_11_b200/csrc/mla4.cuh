@@ -18,9 +18,9 @@
 // that much again, stays in tensor memory as the A operand of S.  It passes through a tile's slot of the ring on its way
 // there.  Tensor memory: O^T in columns 0..255, S in 256..383, Q (512 dims) in 384..511; Q's RoPE dims in shared memory.
 //
-// Warps 0..15: softmax and output (warp w: heads 16 (w % 4) .. + 15, keys 32 (w / 4) .. + 31; a lane holds 16 keys of one
-// head); 8 decode warps: the query rows, and the next tile's 320-byte rows loaded into registers while one is decoded;
-// 2 warps issue the MMAs.  CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a
+// Warps 0..15: query rows, softmax and output (warp w: heads 16 (w % 4) .. + 15, keys 32 (w / 4) .. + 31; a lane holds 16
+// keys of one head); 8 decode warps: the next tile's 320-byte rows loaded into registers while one is decoded; 2 warps
+// issue the MMAs.  CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a
 // range boundary cuts leave fp32 partials for combine4_kernel.
 #pragma once
 #include <cuda_bf16.h>
@@ -61,8 +61,9 @@ constexpr int REGS_LAUNCH = 72, REGS_SM = 72, REGS_DEC = 88, REGS_MMA = 40;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256, TM_Q = 384;
 
-// S complete (and its shared-memory operands free), S read, P written, PV complete; then halves of the ring's slots
-constexpr int B_SFULL = 0, B_SDONE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_FULL = 6, B_EMPTY = B_FULL + 2 * SLOTS;
+// S complete (and its shared-memory operands free), S read, P written, PV complete, query staged; then halves of the slots
+constexpr int B_SFULL = 0, B_SDONE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_QFULL = 5, B_FULL = 6,
+              B_EMPTY = B_FULL + 2 * SLOTS;
 
 // p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
 // maximum m trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     mbar_init(bar(B_SREAD), SM_WARPS);
     mbar_init(bar(B_PFULL), SM_WARPS);
     mbar_init(bar(B_PVDONE), 1);
+    mbar_init(bar(B_QFULL), SM_WARPS);
     for (int i = 0; i < 2 * SLOTS; ++i) {
       mbar_init(bar(B_FULL + i), DEC_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
@@ -438,13 +440,16 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     load_half(0);
     load_half(1);
     slot_next = find_slot(g1);
-    int32_t item = 0, row = g_begin / tpr, row_left = tpr - g_begin % tpr;
-    if (n > 0) {
-      named_bar(2, SM_THREADS + DEC_WARPS * 32);  // the first query row is the softmax warps' work
-      publish(B_FULL);
-      publish(B_FULL + 1);
+    int32_t row = g_begin / tpr, row_left = tpr - g_begin % tpr;
+    // A row's query is the softmax warps' work: here its use of a slot only keeps the barriers' phases in step.
+    auto skip_query = [&] {
+      if (lane == 0) {
+        mbar_arrive(bar(B_FULL + 2 * ring.slot));
+        mbar_arrive(bar(B_FULL + 2 * ring.slot + 1));
+      }
       ring.next();
-    }
+    };
+    if (n > 0) skip_query();
     const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
     for (int32_t i = 0; i < n; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
@@ -477,32 +482,18 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
         }
         publish(B_FULL + 2 * ring.slot + half);
-        if (row_left > 1) load_half(half);  // of the next tile; behind the query where one comes first
+        load_half(half);  // of the next tile
       }
       ring.next();
       slot = slot_next;
       slot_next = find_slot(g2);
       g2 = find_page(t3);
       t3 = position();
-      // the next tile begins a row: its queries first
       if (row_left == 3 && i + 3 < n) q_prefetch(row + 1);
-      if (--row_left == 0 && i + 1 < n) {
+      if (--row_left == 0) {
         row_left = tpr;
         ++row;
-        wait(B_EMPTY + 2 * ring.slot, ring.phase ^ 1);
-        wait(B_EMPTY + 2 * ring.slot + 1, ring.phase ^ 1);
-        uint2 hi[2], lo[2];
-        ++item;
-        q_stage(row, item, ring.slot, 8 * dw, hi[0], lo[0]);
-        q_stage(row, item, ring.slot, 8 * dw + 4, hi[1], lo[1]);
-        wait(B_SDONE, i & 1);
-        q_stage_rope(8 * dw, hi[0], lo[0]);
-        q_stage_rope(8 * dw + 4, hi[1], lo[1]);
-        publish(B_FULL + 2 * ring.slot);
-        publish(B_FULL + 2 * ring.slot + 1);
-        ring.next();
-        load_half(0);
-        load_half(1);
+        if (i + 1 < n) skip_query();
       }
     }
   } else if (warp >= MMA_WARP) {
@@ -515,13 +506,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     const uint32_t lo0 = (base >> 4) | (1u << 16);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     Ring ring;
-    int32_t row_left = 0;
+    int32_t row_left = 0, item = 0;
     if (warp == MMA_WARP) {
       constexpr uint32_t ID_S = make_idesc(0, 1, 0, 0, 128, 128);  // e4m3 q parts, e5m2 keys
       for (int32_t i = 0; i < n; ++i) {
         if (row_left == 0) {  // the row's query to tensor memory, behind the last S that reads the one before
           wait(B_FULL + 2 * ring.slot, ring.phase);
           wait(B_FULL + 2 * ring.slot + 1, ring.phase);
+          wait(B_QFULL, item++ & 1);
           if (i > 0) wait(B_SDONE, (i - 1) & 1);
           tc_fence_after();
           const uint64_t a = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16);
@@ -592,12 +584,15 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   } else {
     // ================================================================= softmax / output warps
     static_assert(REGS_SM == REGS_LAUNCH, "no change");
+    Ring ring;
     if (n > 0) {
       uint2 hi, lo;
       q_stage(g_begin / tpr, 0, 0, 4 * warp, hi, lo);
       q_stage_rope(4 * warp, hi, lo);
       fence_async_smem();
-      asm volatile("bar.arrive 2, %0;" ::"n"(SM_THREADS + DEC_WARPS * 32) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_QFULL));
+      ring.next();
     }
     // Lanes l and l + 16 of a warp hold one head's keys 0..15 and 16..31 of the warp's 32: its scale, maximum and sum are one
     // register each, and a lane's probabilities are 16 consecutive bytes of P.
@@ -708,7 +703,19 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PFULL));
       ++j;
+      ring.next();
       if (!last) continue;
+      if (i + 1 < n) {  // the next row's query, while the last PV runs (S has read the present one)
+        wait(B_EMPTY + 2 * ring.slot, ring.phase ^ 1);
+        wait(B_EMPTY + 2 * ring.slot + 1, ring.phase ^ 1);
+        uint2 hi, lo;
+        q_stage(row + 1, item + 1, ring.slot, 4 * warp, hi, lo);
+        q_stage_rope(4 * warp, hi, lo);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_QFULL));
+        ring.next();
+      }
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
       {
