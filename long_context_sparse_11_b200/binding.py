@@ -169,27 +169,24 @@ def _refuse(detail: str):
     raise DsaError(DSA_ERR_INVALID_ARG, detail)
 
 
-def _on_device(*tensors):
-    """All tensors on the current CUDA device (the library's calls run there, on its current stream)."""
+def _on_device(*tensors) -> int:
+    """All tensors on the current CUDA device, where the library's calls run; that device's current stream."""
     import torch
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            _refuse(f"tensors must be on a CUDA device, got {t.device}")
-        if dev is None:
-            dev = t.device.index
-            if dev != torch.cuda.current_device():
-                _refuse(f"tensor on cuda:{dev}, current device cuda:{torch.cuda.current_device()}")
-        elif t.device.index != dev:
-            _refuse(f"tensors on cuda:{dev} and cuda:{t.device.index}")
+        if t is not None and t.get_device() != dev:
+            _refuse(f"tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        _refuse(f"tensors must be on a CUDA device, got {tensors[0].device}")
+    if dev != torch.cuda.current_device():
+        _refuse(f"tensors on cuda:{dev}, current device cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _i32(t, n: int, name: str):
     """A contiguous int32 vector of n entries (or None)."""
     import torch
-    if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1)):
+    if t is not None and (t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
         _refuse(f"{name} must be a contiguous int32 tensor of {n} entries")
 
 
@@ -343,7 +340,7 @@ def sparse_mla_attn(q, kv: CacheView, idx, k: int, softmax_scale: float, q_rows_
     import torch
     n_q = q.shape[0]
     if kv.dtype == DSA_MXFP4:
-        _check_attn4(q, kv, idx, k, q_rows_per_idx_row, out, lse, workspace)
+        return _sparse_mla_attn4(q, kv, idx, k, softmax_scale, q_rows_per_idx_row, out, lse, workspace)
     out = torch.empty(n_q, 64, 512, dtype=torch.bfloat16, device=q.device) if out is None else out
     lse = torch.empty(n_q, 64, dtype=torch.float32, device=q.device) if lse is None else lse
     lib = load()
@@ -356,23 +353,35 @@ def sparse_mla_attn(q, kv: CacheView, idx, k: int, softmax_scale: float, q_rows_
     return out, lse
 
 
-def _check_attn4(q, kv, idx, k, rows, out, lse, workspace):
-    """The arguments of attention over a 4-bit cache, before their addresses are passed on."""
+def _sparse_mla_attn4(q, kv, idx, k, softmax_scale, rows, out, lse, workspace):
+    """Attention over a 4-bit cache: the arguments are checked before their addresses are passed on."""
     import torch
-    n = q.shape[0]
-    if q.dtype != torch.bfloat16 or q.shape[1:] != (64, 576) or not q.is_contiguous():
+    shape = q.shape
+    if q.dtype is not torch.bfloat16 or shape[1:] != (64, 576) or not q.is_contiguous():
         _refuse("q must be a contiguous bf16 tensor [n_q, 64, 576]")
+    n = shape[0]
     if rows < 1 or n % rows:
         _refuse(f"{n} query rows do not divide into groups of {rows}")
-    if idx.dtype != torch.int32 or idx.shape != (n // rows, k) or not idx.is_contiguous():
+    if idx.dtype is not torch.int32 or idx.shape != (n // rows, k) or not idx.is_contiguous():
         _refuse(f"idx must be a contiguous int32 tensor [{n // rows}, {k}]")
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != (n, 64, 512) or not out.is_contiguous()):
+    if out is None:
+        out = torch.empty(n, 64, 512, dtype=torch.bfloat16, device=q.device)
+    elif out.dtype is not torch.bfloat16 or out.shape != (n, 64, 512) or not out.is_contiguous():
         _refuse("out must be a contiguous bf16 tensor [n_q, 64, 512]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, 64) or not lse.is_contiguous()):
+    if lse is None:
+        lse = torch.empty(n, 64, dtype=torch.float32, device=q.device)
+    elif lse.dtype is not torch.float32 or lse.shape != (n, 64) or not lse.is_contiguous():
         _refuse("lse must be a contiguous fp32 tensor [n_q, 64]")
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         _refuse("workspace must be a contiguous uint8 tensor")
-    _on_device(q, kv._keep[0], idx, out, lse, workspace)
+    stream = _on_device(q, kv._keep[0], idx, out, lse, workspace)
+    lib = load()
+    if workspace is None:
+        need = lib.dsa_sparse_mla_workspace_bytes(n, k, kv)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check(lib.dsa_sparse_mla_attn(q.data_ptr(), kv, idx.data_ptr(), n, rows, k, softmax_scale, out.data_ptr(),
+                                   lse.data_ptr(), workspace.data_ptr(), workspace.numel(), stream))
+    return out, lse
 
 
 ROPE_THETA = 8.0e6
@@ -424,27 +433,31 @@ def rope(x, pos, plan: RopePlan, offset: int = 0, backward: bool = False, out=No
     by default; `out=x` in place).  backward=True is the gradient: rope(grad_out, ..., backward=True) is the
     gradient of x.  Nothing is recorded for autograd."""
     import torch
-    dt = {torch.bfloat16: DSA_BF16, torch.float16: DSA_F16, torch.float32: DSA_F32}.get(x.dtype)
-    if dt is None or x.dim() not in (2, 3):
+    dtype = x.dtype
+    dt = DSA_BF16 if dtype is torch.bfloat16 else DSA_F32 if dtype is torch.float32 else \
+        DSA_F16 if dtype is torch.float16 else -1
+    shape, xs = x.shape, x.stride()
+    dims = len(shape)
+    if dt < 0 or (dims != 3 and dims != 2):
         _refuse("x must be a bf16, fp16 or fp32 tensor [T, H, D] or [T, D]")
     if x.requires_grad and torch.is_grad_enabled():
         _refuse("rope records nothing for autograd: detach x; its gradient is rope(grad, ..., backward=True)")
-    T, D = x.shape[0], x.shape[-1]
-    H = x.shape[1] if x.dim() == 3 else 1
+    T, D = shape[0], shape[-1]
+    H = shape[1] if dims == 3 else 1
     _i32(pos, T, "pos")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    elif out.dtype is not dtype or out.shape != shape:
         _refuse("out must have x's shape and dtype")
-    if D > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1):
+    os_ = out.stride()
+    if D > 1 and (xs[-1] != 1 or os_[-1] != 1):
         _refuse("the last dimension must be contiguous")
-    _on_device(x, pos, out)
-    xh, oh = (x.stride(1), out.stride(1)) if x.dim() == 3 else (D, D)
-    if H == 1:  # the stride of a single head is of no account
-        xh = oh = D
-    xt, ot = (x.stride(0), out.stride(0)) if T > 1 else (H * D, H * D)
-    _check(load().dsa_rope(ctypes.byref(plan), x.data_ptr(), out.data_ptr(), dt, pos.data_ptr(), T, H, D, offset, xt, xh,
-                           ot, oh, 1 if backward else 0, _stream()))
+    stream = _on_device(x, pos, out)
+    # the stride of a single token or head is of no account
+    xh, oh = (xs[1], os_[1]) if H > 1 else (D, D)
+    xt, ot = (xs[0], os_[0]) if T > 1 else (H * xh, H * oh)
+    _check(load().dsa_rope(plan, x.data_ptr(), out.data_ptr(), dt, pos.data_ptr(), T, H, D, offset, xt, xh, ot, oh,
+                           1 if backward else 0, stream))
     return out
 
 
@@ -454,18 +467,19 @@ def latent_append(x, pos, cache: CacheView, gamma=None, eps: float = 1e-6, rope=
     dims, or None), quantised and stored at position pos[r] of sequence seq[r] (r when seq is None), in one launch.
     Each (sequence, position) at most once per call."""
     import torch
-    dt = {torch.bfloat16: DSA_BF16, torch.float32: DSA_F32}.get(x.dtype)
-    if dt is None or x.dim() != 2 or x.shape[1] != 576 or x.stride(1) != 1:
+    dtype, shape, xs = x.dtype, x.shape, x.stride()
+    dt = DSA_BF16 if dtype is torch.bfloat16 else DSA_F32 if dtype is torch.float32 else -1
+    if dt < 0 or len(shape) != 2 or shape[1] != 576 or xs[1] != 1:
         _refuse("x must be a bf16 or fp32 tensor [n, 576] with contiguous rows")
-    n = x.shape[0]
+    n = shape[0]
     _i32(pos, n, "pos")
     _i32(seq, n, "seq")
-    if gamma is not None and (gamma.dtype != torch.float32 or gamma.shape != (512,) or not gamma.is_contiguous()):
+    if gamma is not None and (gamma.dtype is not torch.float32 or gamma.dim() != 1 or gamma.numel() != 512
+                              or not gamma.is_contiguous()):
         _refuse("gamma must be a contiguous fp32 tensor of 512 entries")
-    _on_device(x, pos, seq, gamma, cache._keep[0])
-    _check(load().dsa_latent_append(x.data_ptr(), dt, x.stride(0) if n > 1 else 576, n, _ptr(gamma), eps,
-                                    None if rope is None else ctypes.byref(rope), _ptr(seq), pos.data_ptr(),
-                                    ctypes.byref(cache), _stream()))
+    stream = _on_device(x, pos, seq, gamma, cache._keep[0])
+    _check(load().dsa_latent_append(x.data_ptr(), dt, xs[0] if n > 1 else 576, n, _ptr(gamma), eps, rope, _ptr(seq),
+                                    pos.data_ptr(), cache, stream))
     return cache
 
 
@@ -475,16 +489,16 @@ def latent_read(cache: CacheView, pos, seq=None, out=None):
     import torch
     if pos.dim() != 1:
         _refuse("pos must be a vector")
-    n = pos.shape[0]
+    n = pos.numel()
     _i32(pos, n, "pos")
     _i32(seq, n, "seq")
     if out is None:
         out = torch.empty(n, 576, dtype=torch.bfloat16, device=pos.device)
-    elif out.dtype != torch.bfloat16 or out.shape != (n, 576) or out.stride(1) != 1:
+    elif out.dtype is not torch.bfloat16 or out.shape != (n, 576) or out.stride(1) != 1:
         _refuse("out must be a bf16 tensor [n, 576] with contiguous rows")
-    _on_device(pos, seq, out, cache._keep[0])
-    _check(load().dsa_latent_read(ctypes.byref(cache), _ptr(seq), pos.data_ptr(), n, out.data_ptr(),
-                                  out.stride(0) if n > 1 else 576, _stream()))
+    stream = _on_device(pos, seq, out, cache._keep[0])
+    _check(load().dsa_latent_read(cache, _ptr(seq), pos.data_ptr(), n, out.data_ptr(), out.stride(0) if n > 1 else 576,
+                                  stream))
     return out
 
 

@@ -496,9 +496,13 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   DSA_TRY(cuda_check(cudaGetLastError(), "4-bit sparse MLA launch"));
   if (pl.ws > 0) {
     const int32_t by_row = n_q < pl.grid - 1 ? 1 : 0;
-    const dim3 cg(static_cast<unsigned>(by_row ? n_q : pl.grid - 1), 16, 512 / mla4::COMBINE_THREADS);
-    launch_pdl(mla4::combine4_kernel, cg, mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml, p.tiles_per_row, p.quot,
-               p.rem, pl.grid, by_row, p.out, p.lse);
+    const unsigned cuts = static_cast<unsigned>(by_row ? n_q : pl.grid - 1);
+    if (by_row && n_q * 8 <= pl.grid)  // few rows of 8 and more fragments: more blocks, more fragments in flight
+      launch_pdl(mla4::combine4_kernel<1, 8>, dim3(cuts, 16, 4), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
+                 p.tiles_per_row, p.quot, p.rem, pl.grid, by_row, p.out, p.lse);
+    else
+      launch_pdl(mla4::combine4_kernel<4, 2>, dim3(cuts, 16, 1), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
+                 p.tiles_per_row, p.quot, p.rem, pl.grid, by_row, p.out, p.lse);
     count_launch();
     DSA_TRY(cuda_check(cudaGetLastError(), "4-bit combine launch"));
   }
@@ -1094,6 +1098,10 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t
     p.head_per_cta = n_heads;
   }
   p.head_groups = (n_heads + p.head_per_cta - 1) / p.head_per_cta;
+  p.by_groups = rope::make_div(static_cast<uint32_t>(p.head_groups));
+  p.by_pairs = rope::make_div(static_cast<uint32_t>(p.rot / 2));
+  p.by_units = rope::make_div(static_cast<uint32_t>(per_head));
+  p.by_heads = rope::make_div(static_cast<uint32_t>(p.head_per_cta));
   const int64_t grid = (static_cast<int64_t>(n_tokens) + p.tok_per_cta - 1) / p.tok_per_cta * p.head_groups;
   if (grid > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many tokens x heads");
   const size_t smem = static_cast<size_t>(p.tok_per_cta) * (p.rot / 2) * sizeof(float2);
@@ -1120,6 +1128,7 @@ dsa_status dsa_latent_append(const void* x, int32_t x_dtype, int64_t x_stride, i
     if (rope->rot_dim != lat::ROT) return fail(DSA_ERR_UNSUPPORTED, "latent rows rotate %d dims", lat::ROT);
   }
   if (gamma && (!(eps >= 0.0) || !std::isfinite(eps))) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (gamma && !aligned16(gamma)) return fail(DSA_ERR_INVALID_ARG, "gamma misaligned");
   if (x_stride < lat::DIM || x_stride % (x_dtype == DSA_F32 ? 4 : 8))
     return fail(DSA_ERR_INVALID_ARG, "x_stride %lld invalid", static_cast<long long>(x_stride));
   if (n_rows == 0) return DSA_OK;
@@ -1187,7 +1196,8 @@ dsa_status dsa_latent_read(const dsa_cache_view* cache, const int32_t* seq, cons
   p.batch = cache->batch;
   p.max_pages = cache->max_pages;
   p.n_pages = static_cast<int32_t>(cache->n_tokens / DSA_PAGE);
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + 3) / 4);
+  const int64_t rows = 4 * lat::READ_ROWS;  // per CTA
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + rows - 1) / rows);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cache->dtype == DSA_MXFP4)
     launch_pdl(lat::latent_read_kernel<true>, grid, 288, 0, st, p);

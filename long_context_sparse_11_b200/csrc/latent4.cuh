@@ -52,6 +52,12 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
   return r & 255u;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Eight codes, value i in nibble i, to a word of the row format (the signs move).
 __device__ __forceinline__ uint32_t arrange(uint32_t x) {
   const uint32_t s = x & 0x88888888u;
@@ -107,9 +113,10 @@ __device__ __forceinline__ float load1(const uint8_t* row, int d, bool f32) {
 }
 
 // One warp per row.  Lane l holds values 8l..8l+7 and 256 + 8l.. of the latent dims and pair l of the RoPE dims.
-// The norm and the rotation run in double and are rounded to fp32 once, so that which side of a 4-bit border a
-// value falls on does not depend on the order of a sum; the quantisation is fp32 arithmetic without rounding
-// (power-of-two steps), or the e4m3 rule of dsa_quant_e4m3.
+// The norm and the rotation are formed to 48 bits and more (the sum of squares and the rotation in double, the products in
+// pairs of fp32 numbers, which cost the double unit nothing) and rounded to fp32 once, so that which side of a 4-bit border
+// a value falls on does not depend on the order of a sum; the quantisation is fp32 arithmetic without rounding (power-of-two
+// steps), or the e4m3 rule of dsa_quant_e4m3.
 template <bool F32, bool MX>
 __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constant__ AppendParams p,
                                                             const __grid_constant__ RotFreqs fr) {
@@ -118,12 +125,8 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
   const int lane = threadIdx.x & 31;
   if (r >= p.n_rows) return;
   const int32_t t = p.pos[r];
-  const int64_t slot = slot_of(p.seq ? p.seq[r] : static_cast<int32_t>(r), t, p.block_table, p.batch, p.max_pages,
-                               p.n_pages);
-  if (slot < 0) {
-    if (lane == 0) atomicOr(p.status, DEVERR_BOUNDS);
-    return;
-  }
+  const int32_t b = p.seq ? p.seq[r] : static_cast<int32_t>(r);
+  // the row and gamma are on their way before the page is known
   const uint8_t* row = p.x + r * p.x_stride * (F32 ? 4 : 2);
   float v[2][8];
 #pragma unroll
@@ -146,6 +149,18 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
   }
   const int da = p.half ? NOPE + lane : NOPE + 2 * lane, db = p.half ? NOPE + 32 + lane : NOPE + 2 * lane + 1;
   float ra = load1(row, da, F32), rb = load1(row, db, F32);
+  float g[2][8];
+  if (p.gamma) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(&g[i >> 1][4 * (i & 1)]) =
+          __ldg(reinterpret_cast<const float4*>(p.gamma + 256 * (i >> 1) + 8 * lane + 4 * (i & 1)));
+  }
+  const int64_t slot = slot_of(b, t, p.block_table, p.batch, p.max_pages, p.n_pages);
+  if (slot < 0) {
+    if (lane == 0) atomicOr(p.status, DEVERR_BOUNDS);
+    return;
+  }
   if (p.gamma) {
     double ss = 0.0;
 #pragma unroll
@@ -155,12 +170,16 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const double inv = 1.0 / sqrt(ss * (1.0 / NOPE) + p.eps);
+    const float ih = static_cast<float>(inv), il = static_cast<float>(inv - static_cast<double>(ih));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[i][j] = static_cast<float>(static_cast<double>(v[i][j]) * inv *
-                                     static_cast<double>(p.gamma[256 * i + 8 * lane + j]));
+      for (int j = 0; j < 8; ++j) {
+        const float x = v[i][j];
+        const float gh = ih * g[i][j], gl = fmaf(il, g[i][j], fmaf(ih, g[i][j], -gh));  // inv * gamma as gh + gl
+        const float y = x * gh;
+        v[i][j] = y + fmaf(x, gl, fmaf(x, gh, -y));
+      }
   }
   if (p.rotate) {
     double s, c;
@@ -177,13 +196,8 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float amax = 0.f;
-      bool nan = false;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        amax = fmaxf(amax, fabsf(v[i][j]));
-        nan |= v[i][j] != v[i][j];
-      }
-      if (nan) amax = __uint_as_float(0x7FFFFFFFu);
+      for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[i][j]));
       // the integer order of non-negative floats puts NaN above infinity
       uint32_t u = __float_as_uint(amax);
       u = max(u, __shfl_xor_sync(0xffffffffu, u, 1));
@@ -286,49 +300,72 @@ struct ReadParams {
   int32_t n_rows, batch, max_pages, n_pages;
 };
 
-// One thread per 8 values (72 threads per row): 4 or 8 bytes of codes in, 16 bytes of bf16 out.  4-bit values are
-// exact in bf16; an e4m3 code times its fp32 scale is rounded once.
+// 72 threads per row, 8 values each: 4 or 8 bytes of codes in, 16 bytes of bf16 out; four rows at a time per thread, whose
+// chains of loads (position, page, codes) run side by side.  4-bit values are exact in bf16; an e4m3 code times its fp32
+// scale is rounded once.  Bound by the bytes.
+constexpr int READ_ROWS = 4;
 template <bool MX>
 __global__ void __launch_bounds__(288) latent_read_kernel(const __grid_constant__ ReadParams p) {
   grid_dependency_sync();
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 72;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (4 * READ_ROWS) + threadIdx.x / 72;
   const int w = threadIdx.x % 72;
-  if (r >= p.n_rows) return;
-  const int32_t b = p.seq ? p.seq[r] : static_cast<int32_t>(r), t = p.pos[r];
-  int64_t slot = slot_of(b, t, p.block_table, p.batch, p.max_pages, p.n_pages);
-  if (slot >= 0 && t >= p.seq_lens[b]) slot = -1;
-  if (slot < 0) {
-    if (w == 0) atomicOr(p.status, DEVERR_BOUNDS);
-    return;
-  }
-  float v[8];
-  if (MX) {
-    const uint8_t* row = p.pool + slot * ROW4;
-    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * w));
-    const uint2 m = word_to_e5m2(codes, mag_table(__ldg(row + EXP_OFF + w / 4)));
+  int32_t b[READ_ROWS], t[READ_ROWS];
+  int64_t slot[READ_ROWS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // an e5m2 byte is the high byte of the f16 of the same value
-      const uint32_t by = ((i < 4 ? m.x : m.y) >> (8 * (i & 3))) & 255u;
-      v[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(by << 8)));
+  for (int k = 0; k < READ_ROWS; ++k) {
+    const int64_t r = r0 + 4 * k;
+    const bool in = r < p.n_rows;
+    b[k] = in && p.seq ? p.seq[r] : static_cast<int32_t>(r);
+    t[k] = in ? p.pos[r] : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < READ_ROWS; ++k) {
+    slot[k] = -1;
+    if (r0 + 4 * k >= p.n_rows) continue;
+    slot[k] = slot_of(b[k], t[k], p.block_table, p.batch, p.max_pages, p.n_pages);
+    if (slot[k] >= 0 && t[k] >= p.seq_lens[b[k]]) slot[k] = -1;
+    if (slot[k] < 0 && w == 0) atomicOr(p.status, DEVERR_BOUNDS);
+  }
+  uint2 codes[READ_ROWS];
+  float scale[READ_ROWS];
+  uint32_t ex[READ_ROWS];
+#pragma unroll
+  for (int k = 0; k < READ_ROWS; ++k) {
+    if (slot[k] < 0) continue;
+    if (MX) {
+      const uint8_t* row = p.pool + slot[k] * ROW4;
+      codes[k].x = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * w));
+      ex[k] = __ldg(row + EXP_OFF + w / 4);
+    } else {
+      codes[k] = __ldg(reinterpret_cast<const uint2*>(p.pool + slot[k] * DIM + 8 * w));
+      scale[k] = __ldg(p.scale + slot[k]);
     }
-  } else {
-    const uint2 codes = __ldg(reinterpret_cast<const uint2*>(p.pool + slot * DIM + 8 * w));
-    const float s = __ldg(p.scale + slot);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c2 = ((i < 2 ? codes.x : codes.y) >> (16 * (i & 1))) & 0xFFFFu;
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3);
-      v[2 * i] = __half2float(__ushort_as_half(h.x)) * s;
-      v[2 * i + 1] = __half2float(__ushort_as_half(h.y)) * s;
+  for (int k = 0; k < READ_ROWS; ++k) {
+    if (slot[k] < 0) continue;
+    uint32_t o[4];
+    if (MX) {
+      const uint2 m = word_to_e5m2(codes[k].x, mag_table(ex[k]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // an e5m2 byte is the high byte of the f16 of the same value
+        const uint32_t h2 = __byte_perm(0u, i < 2 ? m.x : m.y, i & 1 ? 0x7060 : 0x5040);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+        const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c2 = ((i < 2 ? codes[k].x : codes[k].y) >> (16 * (i & 1))) & 0xFFFFu;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(__half2float(__ushort_as_half(h.x)) * scale[k],
+                                                       __half2float(__ushort_as_half(h.y)) * scale[k]);
+        o[i] = *reinterpret_cast<const uint32_t*>(&r);
+      }
     }
+    *reinterpret_cast<uint4*>(p.out + (r0 + 4 * k) * p.out_stride + 8 * w) = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p.out + r * p.out_stride + 8 * w) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace lat

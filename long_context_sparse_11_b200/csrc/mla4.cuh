@@ -785,18 +785,20 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block per (4 heads,
-// 128 dims) of a cut row, one dim of 4 heads per thread.  A row has at most 16 fragments (k <= 2,048); one warp forms
-// their weights while the fragments, 8 at a time, are on their way to everyone: one or two memory latencies.
-// blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first inside a row does it).
+// Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block of 128 threads per 4
+// heads of a cut row (DIMS = 4: 4 dims of 4 heads per thread), or per 4 heads and 128 dims (DIMS = 1) when the rows are few
+// and cut into many fragments (at most 16: k <= 2,048).  One warp forms the weights while the first EARLY fragments are on
+// their way to everyone.  blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first
+// inside a row does it).
 constexpr int COMBINE_THREADS = 128;
+template <int DIMS, int EARLY>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* __restrict__ part_o,
                                                                    const float* __restrict__ part_ml, int32_t tpr,
                                                                    int32_t quot, int32_t rem, int32_t grid, int32_t by_row,
                                                                    uint16_t* __restrict__ out, float* __restrict__ lse) {
   grid_dependency_sync();
   __shared__ float wgt[16][4], inv[4];
-  const int32_t hq = blockIdx.y, dim = blockIdx.z * COMBINE_THREADS + threadIdx.x;
+  const int32_t hq = blockIdx.y, dim = (DIMS == 1 ? blockIdx.z * COMBINE_THREADS : 0) + threadIdx.x;
   int32_t row, c;  // the row's first fragment is CTA c - 1's
   if (by_row) {
     row = blockIdx.x;
@@ -812,14 +814,16 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* 
   }
   int32_t n = 2;  // CTA c - 1 (its fragment 1), then CTAs c, c + 1, ... (their fragment 0)
   while (c + n - 1 < grid && range_begin(c + n - 1, quot, rem, grid) < (row + 1) * tpr) ++n;
-  auto frag = [&](int s) { return static_cast<int64_t>(c - 1 + s) * 2 + (s == 0 ? 1 : 0); };
-  constexpr int EARLY = 8;
-  float4 o[EARLY];
+  auto frag = [&](int s) { return (c - 1 + s) * 2 + (s == 0 ? 1 : 0); };
+  float4 o[EARLY][DIMS];
   auto fetch = [&](int s0) {
 #pragma unroll
     for (int u = 0; u < EARLY; ++u)
-      o[u] = s0 + u < n ? reinterpret_cast<const float4*>(part_o)[(frag(s0 + u) * 16 + hq) * 512 + dim]
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int d = 0; d < DIMS; ++d)
+        o[u][d] = s0 + u < n ? reinterpret_cast<const float4*>(part_o)[(static_cast<int64_t>(frag(s0 + u)) * 16 + hq) * 512 +
+                                                                      dim + d * COMBINE_THREADS]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   fetch(0);
   if (threadIdx.x < 32) {  // lane = (fragment, head) of fragments 0..7, and the same of 8..15
@@ -845,28 +849,37 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* 
     for (int d = 4; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
     if (s == 0) {
       inv[e] = L == 0.f ? 0.f : 1.f / L;
-      if (lse && blockIdx.z == 0)
+      if (lse && (DIMS == 4 || blockIdx.z == 0))
         lse[static_cast<int64_t>(row) * 64 + hq * 4 + e] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     }
   }
   __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[DIMS];
+#pragma unroll
+  for (int d = 0; d < DIMS; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < n; s0 += EARLY) {
     if (s0 > 0) fetch(s0);
 #pragma unroll
     for (int u = 0; u < EARLY; ++u) {
+      if (s0 + u >= n) break;
       const float4 w = *reinterpret_cast<const float4*>(wgt[s0 + u]);
-      acc.x = fmaf(w.x, o[u].x, acc.x);
-      acc.y = fmaf(w.y, o[u].y, acc.y);
-      acc.z = fmaf(w.z, o[u].z, acc.z);
-      acc.w = fmaf(w.w, o[u].w, acc.w);
+#pragma unroll
+      for (int d = 0; d < DIMS; ++d) {
+        acc[d].x = fmaf(w.x, o[u][d].x, acc[d].x);
+        acc[d].y = fmaf(w.y, o[u][d].y, acc[d].y);
+        acc[d].z = fmaf(w.z, o[u][d].z, acc[d].z);
+        acc[d].w = fmaf(w.w, o[u][d].w, acc[d].w);
+      }
     }
   }
-  const float a[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat16 v = __float2bfloat16_rn(a[e] * inv[e]);
-    out[(static_cast<int64_t>(row) * 64 + hq * 4 + e) * 512 + dim] = *reinterpret_cast<const uint16_t*>(&v);
+  for (int d = 0; d < DIMS; ++d) {
+    const float a[4] = {acc[d].x, acc[d].y, acc[d].z, acc[d].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat16 v = __float2bfloat16_rn(a[e] * inv[e]);
+      out[(static_cast<int64_t>(row) * 64 + hq * 4 + e) * 512 + dim + d * COMBINE_THREADS] = *reinterpret_cast<const uint16_t*>(&v);
+    }
   }
 }
 

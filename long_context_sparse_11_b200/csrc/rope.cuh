@@ -18,14 +18,52 @@ struct Freqs {
   double f[MAX_PAIRS];
 };
 
-// Sine and cosine of pos * freq.  The reduction subtracts k * 2 pi in two parts (the double nearest to
-// 2 pi and the rest), each in one fused step.
+// Sine and cosine of pos * freq in double, both to about 2^-52.  The reduction to [-pi/4, pi/4] subtracts k * pi/2 in two
+// parts (the double nearest to pi/2 and the rest), each in one fused step; the rest is the Taylor series, whose first term
+// left out is r^17 / 17! <= 5e-17.  About 25 operations: double ones are the scarce kind here.
 __device__ __forceinline__ void sin_cos(int32_t pos, double freq, double& s, double& c) {
   const double a = static_cast<double>(pos) * freq;
-  const double k = rint(a * 0.15915494309189533577);
-  double r = fma(-k, 6.283185307179586232, a);
-  r = fma(-k, 2.4492935982947064e-16, r);
-  sincos(r, &s, &c);
+  const double k = rint(a * 0.63661977236758134308);
+  double r = fma(-k, 1.570796326794896558, a);
+  r = fma(-k, 6.123233995736766036e-17, r);
+  const double q = r * r;
+  double u = -1.0 / 1307674368000.0;  // -1/15!
+  u = fma(u, q, 1.0 / 6227020800.0);
+  u = fma(u, q, -1.0 / 39916800.0);
+  u = fma(u, q, 1.0 / 362880.0);
+  u = fma(u, q, -1.0 / 5040.0);
+  u = fma(u, q, 1.0 / 120.0);
+  u = fma(u, q, -1.0 / 6.0);
+  u = fma(u * q, r, r);
+  double v = 1.0 / 20922789888000.0;  // 1/16!
+  v = fma(v, q, -1.0 / 87178291200.0);
+  v = fma(v, q, 1.0 / 479001600.0);
+  v = fma(v, q, -1.0 / 3628800.0);
+  v = fma(v, q, 1.0 / 40320.0);
+  v = fma(v, q, -1.0 / 720.0);
+  v = fma(v, q, 1.0 / 24.0);
+  v = fma(v, q, -0.5);
+  v = fma(v, q, 1.0);
+  const int n = static_cast<int>(static_cast<long long>(k)) & 3;  // quarter turns
+  s = n & 1 ? v : u;
+  c = n & 1 ? u : v;
+  if (n & 2) s = -s;
+  if ((n + 1) & 2) c = -c;
+}
+
+// Division of numbers below 2^31 by a fixed one, with a multiplication: n / d = (n * mul) >> (32 + shift).
+struct Div {
+  uint32_t d, mul, shift;
+};
+inline Div make_div(uint32_t d) {
+  Div r{d, 0, 0};
+  while ((1ull << (r.shift + 1)) <= d) ++r.shift;  // floor(log2 d)
+  // ceil(2^(32 + shift) / d) for d not a power of two (fits 32 bits); powers of two shift only
+  r.mul = (d & (d - 1)) ? static_cast<uint32_t>(((1ull << (32 + r.shift)) + d - 1) / d) : 0u;
+  return r;
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Div& v) {
+  return v.mul ? __umulhi(n, v.mul) >> v.shift : n >> v.shift;
 }
 
 struct Params {
@@ -35,6 +73,7 @@ struct Params {
   int64_t x_tok, x_head, out_tok, out_head;  // strides in elements
   int32_t n_tokens, n_heads, dim, offset, rot;
   int32_t tok_per_cta, head_per_cta, head_groups;
+  Div by_groups, by_pairs, by_units, by_heads;  // head_groups, rot / 2, 16-byte steps of a head, head_per_cta
   int32_t half;       // 1: pairs (i, i + rot / 2), 0: pairs (2i, 2i + 1)
   int32_t copy_rest;  // 1: the dims outside the rotated ones are copied (out is another tensor than x)
   double sin_sign;    // -1 turns the other way (the gradient)
@@ -69,67 +108,79 @@ union Pack {
   T t[Vec<T>::N];
 };
 
-// One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared
-// memory; then one 16-byte vector (half layout: one of each half) per thread and step.  Bound by the tensor's
-// bytes; each value is rounded once.
+// One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared memory; then
+// each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (16-bit types: 2;
+// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes; each value is
+// rounded once.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p,
                                                        const __grid_constant__ Freqs fr) {
   grid_dependency_sync();
   extern __shared__ float2 cs[];  // [tok_per_cta][rot / 2] (cos, sin), scaled
-  constexpr int V = Vec<T>::N;
-  const int32_t tg = static_cast<int32_t>(blockIdx.x / p.head_groups);
+  constexpr int V = Vec<T>::N, UNROLL = sizeof(T) == 2 ? 2 : 4;
+  const int32_t tg = static_cast<int32_t>(quotient(blockIdx.x, p.by_groups));
   const int32_t t0 = tg * p.tok_per_cta;
-  const int32_t h0 = static_cast<int32_t>(blockIdx.x % p.head_groups) * p.head_per_cta;
+  const int32_t h0 = (static_cast<int32_t>(blockIdx.x) - tg * p.head_groups) * p.head_per_cta;
   const int32_t nt = min(p.tok_per_cta, p.n_tokens - t0), nh = min(p.head_per_cta, p.n_heads - h0);
   const int32_t pairs = p.rot / 2;
   for (int32_t i = threadIdx.x; i < nt * pairs; i += THREADS) {
+    const int32_t t = static_cast<int32_t>(quotient(i, p.by_pairs));
     double s, c;
-    sin_cos(p.pos[t0 + i / pairs], fr.f[i % pairs], s, c);
+    sin_cos(p.pos[t0 + t], fr.f[i - t * pairs], s, c);
     cs[i] = make_float2(static_cast<float>(c * p.mscale), static_cast<float>(s * p.mscale * p.sin_sign));
   }
   __syncthreads();
-  const int32_t turn_units = p.half ? pairs / V : p.rot / V;
-  const int32_t units = turn_units + (p.copy_rest ? (p.dim - p.rot) / V : 0);
-  const int32_t n = nt * nh * units;
-  for (int32_t i = threadIdx.x; i < n; i += THREADS) {
-    const int32_t u = i % units, th = i / units;
-    const int32_t t = th / nh, h = th % nh;
-    const T* src = reinterpret_cast<const T*>(p.x) + (t0 + t) * p.x_tok + (h0 + h) * p.x_head;
-    T* dst = reinterpret_cast<T*>(p.out) + (t0 + t) * p.out_tok + (h0 + h) * p.out_head;
-    if (u >= turn_units) {
-      int32_t d = (u - turn_units) * V;
-      if (d >= p.offset) d += p.rot;
-      *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
-      continue;
+  const int32_t turn_units = p.half ? pairs / V : p.rot / V, units = static_cast<int32_t>(p.by_units.d);
+  const int32_t n = nt * p.head_per_cta * units;  // heads past the last are skipped
+  for (int32_t i0 = threadIdx.x; i0 < n; i0 += THREADS * UNROLL) {
+    Pack<T> a[UNROLL], b[UNROLL];
+    T* dst[UNROLL];
+    int32_t step[UNROLL], tok[UNROLL];  // step < 0: nothing to do
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      const int32_t i = i0 + k * THREADS;
+      const int32_t th = static_cast<int32_t>(quotient(i, p.by_units)), u = i - th * units;
+      const int32_t t = static_cast<int32_t>(quotient(th, p.by_heads)), h = th - t * p.head_per_cta;
+      step[k] = i < n && h < nh ? u : -1;
+      tok[k] = t;
+      if (step[k] < 0) continue;
+      const T* src = reinterpret_cast<const T*>(p.x) + (t0 + t) * p.x_tok + (h0 + h) * p.x_head;
+      dst[k] = reinterpret_cast<T*>(p.out) + (t0 + t) * p.out_tok + (h0 + h) * p.out_head;
+      int32_t d = p.offset + u * V;
+      if (u >= turn_units) {
+        d = (u - turn_units) * V;
+        if (d >= p.offset) d += p.rot;
+      } else if (p.half) {
+        b[k].u = *reinterpret_cast<const uint4*>(src + d + pairs);
+      }
+      a[k].u = *reinterpret_cast<const uint4*>(src + d);
+      dst[k] += d;
     }
-    const float2* ct = cs + t * pairs;
-    if (p.half) {
-      const int32_t d = p.offset + u * V;
-      Pack<T> a, b;
-      a.u = *reinterpret_cast<const uint4*>(src + d);
-      b.u = *reinterpret_cast<const uint4*>(src + d + pairs);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 w = ct[u * V + j];
-        const float xa = to_f32(a.t[j]), xb = to_f32(b.t[j]);
-        a.t[j] = from_f32<T>(xa * w.x - xb * w.y);
-        b.t[j] = from_f32<T>(xa * w.y + xb * w.x);
-      }
-      *reinterpret_cast<uint4*>(dst + d) = a.u;
-      *reinterpret_cast<uint4*>(dst + d + pairs) = b.u;
-    } else {
-      const int32_t d = p.offset + u * V;
-      Pack<T> a;
-      a.u = *reinterpret_cast<const uint4*>(src + d);
+    for (int k = 0; k < UNROLL; ++k) {
+      if (step[k] < 0) continue;
+      if (step[k] < turn_units) {
+        const float2* ct = cs + tok[k] * pairs;
+        if (p.half) {
 #pragma unroll
-      for (int j = 0; j < V; j += 2) {
-        const float2 w = ct[(u * V + j) / 2];
-        const float xa = to_f32(a.t[j]), xb = to_f32(a.t[j + 1]);
-        a.t[j] = from_f32<T>(xa * w.x - xb * w.y);
-        a.t[j + 1] = from_f32<T>(xa * w.y + xb * w.x);
+          for (int j = 0; j < V; ++j) {
+            const float2 w = ct[step[k] * V + j];
+            const float xa = to_f32(a[k].t[j]), xb = to_f32(b[k].t[j]);
+            a[k].t[j] = from_f32<T>(xa * w.x - xb * w.y);
+            b[k].t[j] = from_f32<T>(xa * w.y + xb * w.x);
+          }
+          *reinterpret_cast<uint4*>(dst[k] + pairs) = b[k].u;
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j += 2) {
+            const float2 w = ct[(step[k] * V + j) / 2];
+            const float xa = to_f32(a[k].t[j]), xb = to_f32(a[k].t[j + 1]);
+            a[k].t[j] = from_f32<T>(xa * w.x - xb * w.y);
+            a[k].t[j + 1] = from_f32<T>(xa * w.y + xb * w.x);
+          }
+        }
       }
-      *reinterpret_cast<uint4*>(dst + d) = a.u;
+      *reinterpret_cast<uint4*>(dst[k]) = a[k].u;
     }
   }
 }

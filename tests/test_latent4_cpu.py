@@ -186,7 +186,7 @@ def test_append_and_read_argument_checks(lib):
 
     assert append(rope=wide) == B.DSA_ERR_UNSUPPORTED and append(dt=B.DSA_F16) == B.DSA_ERR_UNSUPPORTED
     for kw in (dict(n=-1), dict(x=None), dict(x=68), dict(stride=512), dict(stride=580), dict(pos=None), dict(eps=-1.0),
-               dict(eps=math.nan)):
+               dict(eps=math.nan), dict(gamma=20)):
         assert append(**kw) == B.DSA_ERR_INVALID_ARG, kw
     for kw in (dict(n=-1), dict(pos=None), dict(out=None), dict(out=68), dict(stride=512), dict(stride=580)):
         assert read(**kw) == B.DSA_ERR_INVALID_ARG, kw
