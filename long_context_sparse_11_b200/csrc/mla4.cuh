@@ -36,13 +36,13 @@ namespace mla4 {
 constexpr int TILE = 128;
 constexpr int SUB = 128 * 128;  // one sub-tile: 128 keys (or q parts) x 128 dims, 1 byte each
 constexpr int RSUB = 128 * 64;  // the RoPE dims of 128 keys (or q parts)
-constexpr int SLOTS = 3;        // of 4 sub-tiles; filled and freed in two halves
+constexpr int SLOTS = 3;        // of 4 sub-tiles
 constexpr int OFF_QR = 0;       // RoPE dims of the 128 q parts
 constexpr int OFF_KV = OFF_QR + RSUB;
 constexpr int OFF_KR = OFF_KV + SLOTS * 4 * SUB;
 constexpr int OFF_P = OFF_KR + RSUB;  // [2 parts][64 heads][128 keys]
 constexpr int OFF_MISC = OFF_P + SUB;
-constexpr int N_BARS = 6 + 4 * SLOTS;
+constexpr int N_BARS = 6 + 2 * SLOTS;
 constexpr int M_TMEM = 208, M_ABORT = 212;
 constexpr int M_MASK = 224;  // uint16 [4 tiles][8 warps]: keys that count
 constexpr int M_ZS = 288;    // float [4 items][64]: logit scale of a head
@@ -61,9 +61,9 @@ constexpr int REGS_LAUNCH = 72, REGS_SM = 72, REGS_DEC = 88, REGS_MMA = 40;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256, TM_Q = 384;
 
-// S complete (and its shared-memory operands free), S read, P written, PV complete, query staged; then halves of the slots
+// S complete (and its shared-memory operands free), S read, P written, PV complete, query staged; then the slots
 constexpr int B_SFULL = 0, B_SDONE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_QFULL = 5, B_FULL = 6,
-              B_EMPTY = B_FULL + 2 * SLOTS;
+              B_EMPTY = B_FULL + SLOTS;
 
 // p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
 // maximum m trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     mbar_init(bar(B_PFULL), SM_WARPS);
     mbar_init(bar(B_PVDONE), 1);
     mbar_init(bar(B_QFULL), SM_WARPS);
-    for (int i = 0; i < 2 * SLOTS; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
       mbar_init(bar(B_FULL + i), DEC_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
     }
@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       }
       ex_a[half] = __ldg(reinterpret_cast<const uint2*>(ra + lat::EXP_OFF + 8 * half));
       ex_b[half] = __ldg(reinterpret_cast<const uint2*>(rb + lat::EXP_OFF + 8 * half));
-      if (half == 1) {
-        raw_r = ld16(rr, 256 + (lane & 1) * 16);
-        ex_r = __ldg(rr + lat::EXP_OFF + 16 + (lane & 1));
-      }
+    };
+    auto load_rope = [&] {
+      raw_r = ld16(rr, 256 + (lane & 1) * 16);
+      ex_r = __ldg(rr + lat::EXP_OFF + 16 + (lane & 1));
     };
 
     auto q_prefetch = [&](int32_t row) {  // 72 lines of this warp's heads
@@ -439,14 +439,12 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     rows_of(slot);
     load_half(0);
     load_half(1);
+    load_rope();
     slot_next = find_slot(g1);
     int32_t row = g_begin / tpr, row_left = tpr - g_begin % tpr;
     // A row's query is the softmax warps' work: here its use of a slot only keeps the barriers' phases in step.
     auto skip_query = [&] {
-      if (lane == 0) {
-        mbar_arrive(bar(B_FULL + 2 * ring.slot));
-        mbar_arrive(bar(B_FULL + 2 * ring.slot + 1));
-      }
+      if (lane == 0) mbar_arrive(bar(B_FULL + ring.slot));
       ring.next();
     };
     if (n > 0) skip_query();
@@ -454,36 +452,31 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     for (int32_t i = 0; i < n; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
       rows_of(slot_next);
+      wait(B_EMPTY + ring.slot, ring.phase ^ 1);
+      if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
+      uint8_t* const dst = smem + OFF_KV + 4 * ring.slot * SUB;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        wait(B_EMPTY + 2 * ring.slot + half, ring.phase ^ 1);
-        if (half == 0) {
-          if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
-        } else if (i >= 1) {
-          wait(B_SDONE, (i - 1) & 1);  // the one RoPE sub-tile
-        }
-#pragma unroll
-        for (int d = 2 * half; d < 2 * half + 2; ++d) {
-          uint4 o0, o1;
-          uint8_t* dst = smem + OFF_KV + (4 * ring.slot + d) * SUB;
-          const uint32_t xa = d & 1 ? ex_a[half].y : ex_a[half].x, xb = d & 1 ? ex_b[half].y : ex_b[half].x;
-          decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
-          *reinterpret_cast<uint4*>(dst + sa) = o0;
-          *reinterpret_cast<uint4*>(dst + sb) = o1;
-          decode32(raw[2 * d + 1], __byte_perm(xb, 0, 0x4440u | c4), o0, o1);
-          *reinterpret_cast<uint4*>(dst + sa + 1024) = o0;  // 8 rows further: the same swizzle
-          *reinterpret_cast<uint4*>(dst + sb + 1024) = o1;
-        }
-        if (half == 1) {
-          uint4 o0, o1;
-          decode32(raw_r, ex_r, o0, o1);
-          const uint32_t o = sw64_off(16 * dw + (lane >> 1), 2 * (lane & 1));
-          *reinterpret_cast<uint4*>(smem + OFF_KR + o) = o0;
-          *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
-        }
-        publish(B_FULL + 2 * ring.slot + half);
-        load_half(half);  // of the next tile
+      for (int d = 0; d < 4; ++d) {
+        uint4 o0, o1;
+        const uint32_t xa = d & 1 ? ex_a[d >> 1].y : ex_a[d >> 1].x, xb = d & 1 ? ex_b[d >> 1].y : ex_b[d >> 1].x;
+        decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
+        *reinterpret_cast<uint4*>(dst + d * SUB + sa) = o0;
+        *reinterpret_cast<uint4*>(dst + d * SUB + sb) = o1;
+        decode32(raw[2 * d + 1], __byte_perm(xb, 0, 0x4440u | c4), o0, o1);
+        *reinterpret_cast<uint4*>(dst + d * SUB + sa + 1024) = o0;  // 8 rows further: the same swizzle
+        *reinterpret_cast<uint4*>(dst + d * SUB + sb + 1024) = o1;
+        if (d & 1) load_half(d >> 1);  // of the next tile
       }
+      if (i >= 1) wait(B_SDONE, (i - 1) & 1);  // the one RoPE sub-tile
+      {
+        uint4 o0, o1;
+        decode32(raw_r, ex_r, o0, o1);
+        const uint32_t o = sw64_off(16 * dw + (lane >> 1), 2 * (lane & 1));
+        *reinterpret_cast<uint4*>(smem + OFF_KR + o) = o0;
+        *reinterpret_cast<uint4*>(smem + OFF_KR + (o ^ 16u)) = o1;
+      }
+      load_rope();
+      publish(B_FULL + ring.slot);
       ring.next();
       slot = slot_next;
       slot_next = find_slot(g2);
@@ -511,8 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       constexpr uint32_t ID_S = make_idesc(0, 1, 0, 0, 128, 128);  // e4m3 q parts, e5m2 keys
       for (int32_t i = 0; i < n; ++i) {
         if (row_left == 0) {  // the row's query to tensor memory, behind the last S that reads the one before
-          wait(B_FULL + 2 * ring.slot, ring.phase);
-          wait(B_FULL + 2 * ring.slot + 1, ring.phase);
+          wait(B_FULL + ring.slot, ring.phase);
           wait(B_QFULL, item++ & 1);
           if (i > 0) wait(B_SDONE, (i - 1) & 1);
           tc_fence_after();
@@ -520,8 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < 16; ++c) tmem_copy(tm + TM_Q + 8 * c, a + (c >> 2) * (SUB / 16) + 2 * (c & 3));
-            mma_commit(bar(B_EMPTY + 2 * ring.slot));
-            mma_commit(bar(B_EMPTY + 2 * ring.slot + 1));
+            mma_commit(bar(B_EMPTY + ring.slot));
           }
           __syncwarp();
           ring.next();
@@ -529,27 +520,21 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         }
         --row_left;
         if (i > 0) wait(B_SREAD, (i - 1) & 1);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          wait(B_FULL + 2 * ring.slot + half, ring.phase);
-          tc_fence_after();
-          const uint64_t b = desc128(lo0 + (OFF_KV + (4 * ring.slot + 2 * half) * SUB) / 16);
-          const uint32_t a = tm + TM_Q + 64 * half, keep = half;
-          if (elect_one()) {
+        wait(B_FULL + ring.slot, ring.phase);
+        tc_fence_after();
+        const uint64_t b = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16);
+        const uint64_t ar = desc64(lo0 + OFF_QR / 16), br = desc64(lo0 + OFF_KR / 16);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_f8_ta(tm + TM_S, a + 8 * kk, b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S, kk > 0 ? 1u : keep);
-            if (half == 1) {
-              const uint64_t ar = desc64(lo0 + OFF_QR / 16), br = desc64(lo0 + OFF_KR / 16);
-              mma_f8(tm + TM_S, ar, br, ID_S, 1);
-              mma_f8(tm + TM_S, ar + 2, br + 2, ID_S, 1);
-              mma_commit(bar(B_SFULL));
-              mma_commit(bar(B_SDONE));
-              mbar_arrive(bar(B_SFULL));  // and what the decode warps left in shared memory (masks, scales)
-            }
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 16; ++kk)
+            mma_f8_ta(tm + TM_S, tm + TM_Q + 8 * kk, b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S, kk > 0);
+          mma_f8(tm + TM_S, ar, br, ID_S, 1);
+          mma_f8(tm + TM_S, ar + 2, br + 2, ID_S, 1);
+          mma_commit(bar(B_SFULL));
+          mma_commit(bar(B_SDONE));
+          mbar_arrive(bar(B_SFULL));  // and what the decode warps left in shared memory (masks)
         }
+        __syncwarp();
         ring.next();
       }
     } else if (warp == MMA_WARP + 1) {
@@ -573,8 +558,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
               mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + 2 * kk, ID_PV, kk > 0 ? 1u : keep);
               mma_f8(tm + 64u * mb, a + mb * (SUB / 16) + 256 * kk, b + RSUB / 16 + 2 * kk, ID_PVR, 1);
             }
-            if (mb & 1) mma_commit(bar(B_EMPTY + 2 * ring.slot + (mb >> 1)));
           }
+          mma_commit(bar(B_EMPTY + ring.slot));
           mma_commit(bar(B_PVDONE));
         }
         __syncwarp();
@@ -706,8 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       ring.next();
       if (!last) continue;
       if (i + 1 < n) {  // the next row's query, while the last PV runs (S has read the present one)
-        wait(B_EMPTY + 2 * ring.slot, ring.phase ^ 1);
-        wait(B_EMPTY + 2 * ring.slot + 1, ring.phase ^ 1);
+        wait(B_EMPTY + ring.slot, ring.phase ^ 1);
         uint2 hi, lo;
         q_stage(row + 1, item + 1, ring.slot, 4 * warp, hi, lo);
         q_stage_rope(4 * warp, hi, lo);
