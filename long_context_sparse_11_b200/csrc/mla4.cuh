@@ -61,8 +61,8 @@ constexpr int REGS_LAUNCH = 72, REGS_SM = 72, REGS_DEC = 88, REGS_MMA = 40;
 static_assert(SM_THREADS * REGS_SM + DEC_WARPS * 32 * REGS_DEC + 128 * REGS_MMA <= THREADS * REGS_LAUNCH, "register split");
 constexpr uint32_t TM_S = 256, TM_Q = 384;
 
-// S complete (and its shared-memory operands free), S read, P written, PV complete, query staged; then the slots
-constexpr int B_SFULL = 0, B_SDONE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_QFULL = 5, B_FULL = 6,
+// S complete, its RoPE operand free, S read, P written, PV complete, query staged; then the slots
+constexpr int B_SFULL = 0, B_RFREE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, B_QFULL = 5, B_FULL = 6,
               B_EMPTY = B_FULL + SLOTS;
 
 // p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
@@ -103,6 +103,9 @@ __device__ __forceinline__ uint32_t sw64_off(uint32_t r, uint32_t c) { return r 
 __device__ __forceinline__ int32_t range_begin(int32_t c, int32_t quot, int32_t rem, int32_t grid) {
   return c * quot + c * rem / grid;
 }
+
+// Keeps the arithmetic on loaded registers behind this point (moved up, it would wait for loads just issued).
+__device__ __forceinline__ void pin(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
 
 // One block of 32 values (16 bytes) to its e5m2 bytes.
 __device__ __forceinline__ void decode32(const uint4& raw, uint32_t exp_byte, uint4& o0, uint4& o1) {
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   }
   if (threadIdx.x == 0) {
     mbar_init(bar(B_SFULL), 2);
-    mbar_init(bar(B_SDONE), 1);
+    mbar_init(bar(B_RFREE), 1);
     mbar_init(bar(B_SREAD), SM_WARPS);
     mbar_init(bar(B_PFULL), SM_WARPS);
     mbar_init(bar(B_PVDONE), 1);
@@ -458,6 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         uint4 o0, o1;
+        pin(raw[2 * d]), pin(raw[2 * d + 1]);
         const uint32_t xa = d & 1 ? ex_a[d >> 1].y : ex_a[d >> 1].x, xb = d & 1 ? ex_b[d >> 1].y : ex_b[d >> 1].x;
         decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
         *reinterpret_cast<uint4*>(dst + d * SUB + sa) = o0;
@@ -467,9 +471,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         *reinterpret_cast<uint4*>(dst + d * SUB + sb + 1024) = o1;
         if (d & 1) load_half(d >> 1);  // of the next tile
       }
-      if (i >= 1) wait(B_SDONE, (i - 1) & 1);  // the one RoPE sub-tile
+      if (i >= 1) wait(B_RFREE, (i - 1) & 1);  // the one RoPE sub-tile
       {
         uint4 o0, o1;
+        pin(raw_r);
         decode32(raw_r, ex_r, o0, o1);
         const uint32_t o = sw64_off(16 * dw + (lane >> 1), 2 * (lane & 1));
         *reinterpret_cast<uint4*>(smem + OFF_KR + o) = o0;
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         if (row_left == 0) {  // the row's query to tensor memory, behind the last S that reads the one before
           wait(B_FULL + ring.slot, ring.phase);
           wait(B_QFULL, item++ & 1);
-          if (i > 0) wait(B_SDONE, (i - 1) & 1);
+          if (i > 0) wait(B_SFULL, (i - 1) & 1);
           tc_fence_after();
           const uint64_t a = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16);
           if (elect_one()) {
@@ -525,13 +530,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         const uint64_t b = desc128(lo0 + (OFF_KV + 4 * ring.slot * SUB) / 16);
         const uint64_t ar = desc64(lo0 + OFF_QR / 16), br = desc64(lo0 + OFF_KR / 16);
         if (elect_one()) {
+          // the RoPE dims first: their one buffer is then free for the next tile while the rest runs
+          mma_f8(tm + TM_S, ar, br, ID_S, 0);
+          mma_f8(tm + TM_S, ar + 2, br + 2, ID_S, 1);
+          mma_commit(bar(B_RFREE));
 #pragma unroll
           for (int kk = 0; kk < 16; ++kk)
-            mma_f8_ta(tm + TM_S, tm + TM_Q + 8 * kk, b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S, kk > 0);
-          mma_f8(tm + TM_S, ar, br, ID_S, 1);
-          mma_f8(tm + TM_S, ar + 2, br + 2, ID_S, 1);
+            mma_f8_ta(tm + TM_S, tm + TM_Q + 8 * kk, b + (kk >> 2) * (SUB / 16) + 2 * (kk & 3), ID_S, 1);
           mma_commit(bar(B_SFULL));
-          mma_commit(bar(B_SDONE));
           mbar_arrive(bar(B_SFULL));  // and what the decode warps left in shared memory (masks)
         }
         __syncwarp();
