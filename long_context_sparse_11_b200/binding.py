@@ -239,6 +239,8 @@ def _check_pool4(pool, block_table, seq_lens):
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
         _refuse("block_table must be a contiguous int32 tensor [sequences, max_pages]")
     _i32(seq_lens, block_table.shape[0], "seq_lens")
+    if not pool.device == block_table.device == seq_lens.device:
+        _refuse(f"pool, block_table and seq_lens on {pool.device}, {block_table.device} and {seq_lens.device}")
 
 
 def latent_pool4(n_pages: int, device="cuda"):

@@ -250,6 +250,28 @@ dsa_status check_latent_pages(const dsa_cache_view* v) {
   return check_view(&c, DSA_DQK, "cache");
 }
 
+// Whether a head's dims of x and of out share memory.  Where the tensors' extents meet, only two slices of one
+// tensor (equal strides, the outer a multiple of the inner) are told apart; anything else counts as an overlap.
+bool rope_overlap(const void* x, const void* out, int64_t es, int64_t n_tokens, int64_t n_heads, int64_t dim,
+                  int64_t x_tok, int64_t x_head, int64_t out_tok, int64_t out_head) {
+  if (n_tokens == 1) x_tok = out_tok = 0;
+  if (n_heads == 1) x_head = out_head = 0;
+  auto low = [&](int64_t tok, int64_t head) {
+    return std::min<int64_t>(0, (n_tokens - 1) * tok) + std::min<int64_t>(0, (n_heads - 1) * head);
+  };
+  auto high = [&](int64_t tok, int64_t head) {
+    return std::max<int64_t>(0, (n_tokens - 1) * tok) + std::max<int64_t>(0, (n_heads - 1) * head) + dim;
+  };
+  const int64_t delta = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(x)) / es;
+  if (delta + low(out_tok, out_head) >= high(x_tok, x_head) || low(x_tok, x_head) >= delta + high(out_tok, out_head))
+    return false;
+  int64_t inner = std::min(out_tok, out_head), outer = std::max(out_tok, out_head);
+  if (inner == 0) inner = outer;  // a single head or a single token
+  if (x_tok != out_tok || x_head != out_head || inner <= 0 || outer % inner) return true;
+  const int64_t at = (delta % inner + inner) % inner;
+  return at < dim || inner - at < dim;
+}
+
 dsa_status check_rope_plan(const dsa_rope_plan* p) {
   if (!p) return fail(DSA_ERR_INVALID_ARG, "null rope plan");
   if (p->rot_dim < 16 || p->rot_dim > 2 * DSA_ROPE_MAX_PAIRS || p->rot_dim % 16 ||
@@ -1070,6 +1092,9 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t
       (n_tokens > 1 && out_token_stride < (n_heads - 1) * out_head_stride + dim &&
        !(n_heads > 1 && out_head_stride >= (n_tokens - 1) * out_token_stride + dim && out_token_stride >= dim)))
     return fail(DSA_ERR_INVALID_ARG, "out's tokens or heads overlap");
+  if (x != out && rope_overlap(x, out, dtype == DSA_F32 ? 4 : 2, n_tokens, n_heads, dim, x_token_stride, x_head_stride,
+                               out_token_stride, out_head_stride))
+    return fail(DSA_ERR_INVALID_ARG, "out overlaps x (only out == x works in place)");
   DeviceState* ds = nullptr;
   DSA_TRY(device_state(&ds));
   rope::Params p{};

@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const double inv = 1.0 / sqrt(ss * (1.0 / NOPE) + p.eps);
     const float ih = static_cast<float>(inv), il = static_cast<float>(inv - static_cast<double>(ih));
+    float probe = 0.f;  // NaN once a result is not finite
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -179,7 +180,17 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
         const float gh = ih * g[i][j], gl = fmaf(il, g[i][j], fmaf(ih, g[i][j], -gh));  // inv * gamma as gh + gl
         const float y = x * gh;
         v[i][j] = y + fmaf(x, gl, fmaf(x, gh, -y));
+        probe = fmaf(v[i][j], 0.f, probe);
       }
+    // Where the pairs leave fp32's range (a result or 1 / rms above it, a subnormal 1 / rms): the products in double
+    if (probe != 0.f || ih < 1e-25f) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = static_cast<float>(static_cast<double>(load1(row, 256 * i + 8 * lane + j, F32)) * inv *
+                                       static_cast<double>(g[i][j]));
+    }
   }
   if (p.rotate) {
     double s, c;

@@ -708,20 +708,17 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       }
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
       ++item;
-      {
-        const float2 v = unpack2(lsum);
-        float l = v.x + v.y;
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (upper == 0) red[grp * 64 + head] = l;
-      }
-      wait(B_PVDONE, i & 1);
+      float l = unpack2(lsum).x + unpack2(lsum).y;
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      wait(B_PVDONE, i & 1);  // every warp has written P, so none still reads its tile's maxima in red
       tc_fence_after();
+      if (upper == 0) red[grp * 64 + head] = l;
       named_bar(1, SM_THREADS);
       const int32_t row0 = row * tpr;  // this row's first global tile
       const bool whole = row0 >= g_begin && row0 + tpr <= g_end;
       const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
       if (grp == 0 && upper == 0) {
-        const float l = 256.f * (red[head] + red[64 + head] + red[128 + head] + red[192 + head]);  // sum of p
+        l = 256.f * (red[head] + red[64 + head] + red[128 + head] + red[192 + head]);  // sum of p
         alpha[head] = l == 0.f ? 0.f : 1.f / l;
         if (!whole) {
           p.part_ml[pr * 128 + head] = l == 0.f ? -INFINITY : -nn - 8.f;

@@ -510,6 +510,202 @@ def test_attention_is_repeatable_captured_and_on_other_streams():
     check_attention(q2, kv, idx, rows, o, e)
 
 
+def test_rope_between_slices_of_one_tensor_and_far_apart_rows():
+    rng = np.random.default_rng(15)
+    buf = torch.from_numpy(rng.normal(size=(9, 4, 128))).bfloat16().cuda()
+    pos, plan = i32_dev(rng.integers(0, 1 << 20, size=9)), dsa.RopePlan(64)
+    want = dsa.rope(buf[..., :64].contiguous(), pos, plan)
+    dsa.rope(buf[..., :64], pos, plan, out=buf[..., 64:])       # interleaved in memory, no shared byte
+    assert torch.equal(buf[..., 64:], want)
+    big = torch.zeros((1 << 31) + 4096, dtype=torch.bfloat16, device="cuda")
+    far = big.as_strided((3, 2, 64), (1 << 30, 64, 1))          # token 2 starts at element 2^31
+    far.copy_(buf[:3, :2, :64])
+    got = dsa.rope(far, pos[:3], plan)
+    assert torch.equal(got, want[:3, :2])
+    dsa.rope(far, pos[:3], plan, out=far)
+    assert torch.equal(far, got)
+    dsa.sync_status()
+
+
+@pytest.mark.parametrize("mx", [True, False])
+def test_append_of_rows_at_the_ends_of_the_fp32_range(mx):
+    """Sums of squares, reciprocals and products beyond fp32 where the result is not, or saturates."""
+    rng = np.random.default_rng(16)
+    n = 7
+    x = rng.normal(size=(n, 576)).astype(np.float32)
+    gamma = (1 + 0.2 * rng.normal(size=512)).astype(np.float32)
+    x[0] *= np.float32(1e37)
+    x[1, :512] *= np.float32(2.0 ** -130)                        # subnormal, normalised with eps = 0
+    x[2, :512] *= np.float32(2.0 ** -147)
+    if mx:
+        x[3, 7] = np.inf
+        x[4, :512] = 0.0                                         # 0 / 0
+        gamma[40:48] = 3e38                                      # results past fp32 saturate
+    x[5, :500] = 0.0
+    x[6, :512] *= np.float32(2.0 ** 100)
+    n_pages, bt = paged(rng, [n])
+    seq, pos = np.zeros(n, dtype=np.int32), np.arange(n, dtype=np.int32)
+    f, m = L4.inv_freq(64, 8.0e6)
+    with np.errstate(all="ignore"):
+        y = L4.latent_rows(x, gamma, 0.0, pos, f)
+    xt, slots = torch.from_numpy(x).cuda(), bt[0, 0].astype(np.int64) * 64 + pos
+    kw = dict(gamma=f32_dev(gamma), eps=0.0, rope=dsa.RopePlan(64), seq=i32_dev(seq))
+    if mx:
+        pool = garbage_pool(n_pages)
+        pd = u8_dev(pool)
+        dsa.latent_append(xt, i32_dev(pos), dsa.paged_view(pd, None, i32_dev(bt), i32_dev([n])), **kw)
+        dsa.sync_status()
+        assert np.array_equal(pd.cpu().numpy(), L4.append(pool, y, bt, seq, pos))
+    else:
+        s = (np.abs(y).max(-1) / np.float32(448.0)).astype(np.float32)
+        codes = torch.from_numpy(y / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+        pd = torch.zeros(n_pages, 64, 576, dtype=torch.uint8, device="cuda")
+        sd = torch.zeros(n_pages, 64, device="cuda")
+        dsa.latent_append(xt, i32_dev(pos), dsa.paged_view(pd, sd, i32_dev(bt), i32_dev([n])), **kw)
+        dsa.sync_status()
+        assert np.array_equal(pd.cpu().numpy().reshape(-1, 576)[slots], codes)
+        assert np.array_equal(sd.cpu().numpy().reshape(-1)[slots], s)
+
+
+def test_a_pool_beyond_32_bit_offsets():
+    """Pages whose bytes lie past 2^32: appended to, read back and attended to like any other."""
+    rng = np.random.default_rng(17)
+    n_pages, n, k = 215000, 130, 130                             # 4.4 GB
+    pool = dsa.latent_pool4(n_pages)
+    bt = np.array([[n_pages - 1, 3, n_pages - 2]], dtype=np.int32)
+    view = dsa.paged_view(pool, None, i32_dev(bt), i32_dev([n]))
+    x = torch.from_numpy(rng.normal(size=(n, 576))).bfloat16().cuda()
+    pos, seq = i32_dev(np.arange(n)), torch.zeros(n, dtype=torch.int32, device="cuda")
+    dsa.latent_append(x, pos, view, seq=seq)
+    kv = L4.decode_rows(L4.encode_rows(f64(x).astype(np.float32)))
+    assert np.array_equal(f64(dsa.latent_read(view, pos, seq=seq)), kv)
+    idx = rng.permutation(n)[None].astype(np.int32)
+    qd = torch.from_numpy(rng.normal(size=(2, 64, 576))).bfloat16().cuda()
+    out, lse = dsa.sparse_mla_attn(qd, view, i32_dev(idx), k, SCALE, 2)
+    dsa.sync_status()
+    check_attention(qd, [kv], idx, 2, out, lse)
+    assert int(pool[:3].max()) == 0 and int(pool[4:1000].max()) == 0 and int(pool[-1000:-2].max()) == 0
+
+
+def test_attention_over_many_short_rows():
+    """More rows than SMs by far, one tile and two tiles each."""
+    rng = np.random.default_rng(18)
+    for lens, rows, k in (([40] * 700, 3, 33), ([200] * 331, 2, 131)):
+        idx = selection(rng, lens, k)
+        idx[5] = -1
+        qd, _, kv, out, lse = run_attention(rng, lens, rows, k, idx)
+        dsa.sync_status()
+        check_attention(qd, kv, idx, rows, out, lse)
+
+
+def test_two_attentions_at_once_on_streams_of_their_own():
+    rng = np.random.default_rng(19)
+    calls = []
+    for lens, rows, k in (([2600] * 9, 3, 2048), ([900] * 40, 1, 700)):
+        idx = selection(rng, lens, k)
+        qd, view, kv, out, lse = run_attention(rng, lens, rows, k, idx)
+        calls.append((qd, view, i32_dev(idx), k, rows, out, lse, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for qd, view, idx, k, rows, out, lse, st in calls:
+            with torch.cuda.stream(st):
+                got.append(dsa.sparse_mla_attn(qd, view, idx, k, SCALE, rows) + (out, lse))
+    torch.cuda.synchronize()
+    dsa.sync_status()
+    for o, e, out, lse in got:
+        assert torch.equal(o, out) and torch.equal(e, lse)
+
+
+def test_attention_refuses_a_workspace_that_is_too_small_or_misaligned():
+    rng = np.random.default_rng(20)
+    lens, k = [600] * 2, 512
+    qd, view, kv, out, lse = run_attention(rng, lens, 1, k, selection(rng, lens, k))
+    idx = i32_dev(selection(rng, lens, k))
+    need = dsa.sparse_mla_workspace_bytes(2, k, view)
+    assert need > 0
+    for ws in (torch.empty(need - 16, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 16, dtype=torch.uint8, device="cuda")[8:]):
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.sparse_mla_attn(qd, view, idx, k, SCALE, workspace=ws)
+        assert e.value.status == 6
+    dsa.sync_status()
+
+
+def test_parts_of_a_selection_merge_to_the_whole():
+    """Split over ranks: each part's bf16 output and its lse, joined by dsa_combine_partials.  The joined output is a mean of
+    the parts' with weights that carry the parts' lse errors, rounded to bf16 once more."""
+    rng = np.random.default_rng(21)
+    lens, k = [1500] * 3, 1024
+    idx = selection(rng, lens, k)
+    halves = [np.where(np.arange(k) % 2 == g, idx, -1).astype(np.int32) for g in range(2)]
+    halves[0][2], halves[1][2] = idx[2], -1                      # a part without a key
+    qd, view, kv, _, _ = run_attention(rng, lens, 1, k, idx)
+    parts = [dsa.sparse_mla_attn(qd, view, i32_dev(h), k, SCALE) for h in halves]
+    out, lse = dsa.combine_partials(torch.stack([p[0] for p in parts]), torch.stack([p[1] for p in parts]))
+    dsa.sync_status()
+    o, e = f64(out), f64(lse)
+    for b in range(3):
+        ro, rl, _, _ = reference(f64(qd[b:b + 1]), kv[b], idx[b])
+        bound, lse_bound = np.zeros_like(ro), np.zeros_like(rl)
+        for h in halves:
+            po, pl, bo, bl = reference(f64(qd[b:b + 1]), kv[b], h[b])
+            w = np.exp(pl - rl)[..., None]
+            lse_bound = np.maximum(lse_bound, bl)
+            bound += w * ((1 + 3 * bl[..., None]) * bo + 3 * bl[..., None] * np.abs(po - ro))
+        assert np.all(np.abs(o[b] - ro[0]) <= bound[0] + 2.0 ** -8 * (np.abs(ro[0]) + bound[0]) + 2.0 ** -20)
+        assert np.all(np.abs(e[b] - rl[0]) <= lse_bound[0] + 2.0 ** -18)
+
+
+def test_rope_append_read_and_attention_in_one_graph():
+    """Captured together and replayed on other rows, positions and lengths."""
+    rng = np.random.default_rng(22)
+    n_seqs, k = 3, 192
+    n_pages, bt = paged(rng, [400] * n_seqs)
+    plan = dsa.RopePlan(64, layout="half")
+    gamma = f32_dev((1 + 0.2 * rng.normal(size=512)).astype(np.float32))
+    lens, pos = i32_dev([1] * n_seqs), i32_dev([0] * n_seqs)
+    x = torch.zeros(n_seqs, 576, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(n_seqs, 64, 576, dtype=torch.bfloat16, device="cuda")
+    idx = i32_dev(np.full((n_seqs, k), -1))
+
+    def step(view, x, q, pos, idx, out):
+        dsa.latent_append(x, pos, view, gamma=gamma, rope=plan)
+        dsa.rope(q, pos, plan, offset=512, out=out["q"])
+        dsa.sparse_mla_attn(out["q"], view, idx, k, SCALE, out=out["o"], lse=out["lse"], workspace=out["ws"])
+        dsa.latent_read(view, pos, out=out["rows"])
+
+    def buffers(view):
+        return dict(q=torch.empty_like(q), o=torch.empty(n_seqs, 64, 512, dtype=torch.bfloat16, device="cuda"),
+                    lse=torch.empty(n_seqs, 64, device="cuda"), rows=torch.empty_like(x),
+                    ws=torch.empty(max(16, dsa.sparse_mla_workspace_bytes(n_seqs, k, view)), dtype=torch.uint8,
+                                   device="cuda"))
+
+    views = [dsa.paged_view(dsa.latent_pool4(n_pages), None, i32_dev(bt), lens) for _ in range(2)]
+    eager, graphed = buffers(views[0]), buffers(views[1])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step(views[1], x, q, pos, idx, graphed)
+    for t in range(4):
+        x.copy_(torch.from_numpy(rng.normal(size=(n_seqs, 576))))
+        q.copy_(torch.from_numpy(rng.normal(size=(n_seqs, 64, 576))))
+        at = t * np.arange(1, n_seqs + 1)
+        pos.copy_(torch.from_numpy(at.astype(np.int32)))
+        lens.copy_(torch.from_numpy((at + 1).astype(np.int32)))
+        sel = np.full((n_seqs, k), -1, dtype=np.int32)
+        for b in range(n_seqs):
+            sel[b, :at[b] + 1] = rng.permutation(int(at[b]) + 1)
+        idx.copy_(torch.from_numpy(sel))
+        step(views[0], x, q, pos, idx, eager)
+        graph.replay()
+        dsa.sync_status()
+        for name in ("q", "o", "lse", "rows"):
+            assert torch.equal(eager[name], graphed[name]), (t, name)
+        assert torch.equal(views[0]._keep[0], views[1]._keep[0])
+        assert bool(torch.isfinite(eager["o"]).all())
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 

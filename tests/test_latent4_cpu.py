@@ -229,3 +229,28 @@ def test_four_bit_tensor_checks(lib):
     _refused(lambda: dsa.sparse_mla_attn(q, v, idx, 8, 0.04, q_rows_per_idx_row=0))
     _refused(lambda: dsa.sparse_mla_attn(q, v, idx, 8, 0.04, out=torch.zeros(2, 64, 512)))
     assert "CUDA" in _refused(lambda: dsa.sparse_mla_attn(q, v, idx, 8, 0.04))
+
+
+def test_rope_refuses_outputs_that_overlap_the_input(lib):
+    """Only overlaps are called here: what is accepted would be launched."""
+    plan = dsa.RopePlan(64)
+
+    def call(out, T=2, H=4, D=128, xs=(512, 128), os_=(512, 128), x=64, dt=B.DSA_BF16):
+        rc = lib.dsa_rope(ctypes.byref(plan), x, out, dt, 16, T, H, D, 0, xs[0], xs[1], os_[0], os_[1], 0, None)
+        return rc, lib.dsa_last_error()
+
+    for out, kw in ((64 + 16, {}), (64 + 256, {}), (64 + 2048 - 16, {}), (64 + 1024, dict(os_=(1024, 256))),
+                    (64 + 16, dict(T=1, H=1)), (64 + 256, dict(T=1)),
+                    (64 + 512 - 16, dict(D=256, H=1, xs=(256, 0), os_=(256, 0))),
+                    (64 + 64, dict(D=64)), (64 + 256 - 16, dict(D=64)), (64 + 256, dict(dt=B.DSA_F32)),
+                    (64 + 128, dict(H=2, T=4, D=64, xs=(64, 512), os_=(64, 512)))):
+        rc, msg = call(out, **kw)
+        assert rc == B.DSA_ERR_INVALID_ARG and b"overlaps x" in msg, (out, kw, rc, msg)
+        rc, msg = call(64, x=out, **{**kw, "xs": kw.get("os_", (512, 128)), "os_": kw.get("xs", (512, 128))})
+        assert rc == B.DSA_ERR_INVALID_ARG and b"overlap" in msg, (out, kw, rc, msg)
+
+
+def test_four_bit_views_lie_on_one_device(lib):
+    pool, bt, lens = dsa.latent_pool4(4, "cpu"), torch.zeros(2, 2, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    assert "meta" in _refused(lambda: dsa.paged_view(pool, None, bt, lens.to("meta")))
+    assert "meta" in _refused(lambda: dsa.paged_view(pool, None, bt.to("meta"), lens))
