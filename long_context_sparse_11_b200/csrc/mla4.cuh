@@ -353,10 +353,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   if (warp >= SM_WARPS && warp < MMA_WARP) {
     // ================================================================= decode warps
     regs_inc<REGS_DEC>();
-    // Warp dw holds keys 16 dw .. 16 dw + 15 of every tile.  Latent sub-tile d: lane l decodes blocks 4 d + l % 4 of
-    // keys l / 4 and l / 4 + 8 (64 consecutive bytes of a row per four lanes); RoPE: block 16 + l % 2 of key l / 2.
+    // Warp dw holds keys 16 dw .. 16 dw + 15 of every tile.  Latent dims: lane l decodes block `blk` of keys 2 k + `odd`, k = 0..7
+    // (256 consecutive bytes of two rows in a load: what these loads cost is the lines they touch); RoPE: block 16 + l % 2 of
+    // key l / 2.  Eight neighbouring lanes store to 128 different bytes modulo 128: four chunks of an even row, four of an odd.
     const int dw = warp - SM_WARPS;
-    const int c4 = lane & 3, r4 = lane >> 2;
+    const int blk = (lane & 3) | ((lane >> 3) << 2), odd = (lane >> 2) & 1;
     auto publish = [&](int b) {  // this warp's stores are visible to the tensor core, then one arrival
       fence_async_smem();
       __syncwarp();
@@ -403,26 +404,18 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       return g.page * 64 + (g.t & 63);
     };
     uint4 raw[8], raw_r;
-    uint2 ex_a[2], ex_b[2];
-    uint32_t ex_r;
+    uint32_t ex[8], ex_r;
     auto row_ptr = [&](int32_t slot, int src) -> const uint8_t* {  // a key that does not count reads a row of zeros
       const int32_t s = __shfl_sync(0xffffffffu, slot, src);
       return s < 0 ? zero_row : p.kv + static_cast<int64_t>(s) * lat::ROW4;
     };
     auto ld16 = [&](const uint8_t* r, int off) { return __ldg(reinterpret_cast<const uint4*>(r + off)); };
 
-    const uint8_t *ra, *rb, *rr;  // rows of this lane's blocks
-    auto rows_of = [&](int32_t slots) {
-      ra = row_ptr(slots, r4), rb = row_ptr(slots, r4 + 8), rr = row_ptr(slots, lane >> 1);
-    };
-    auto load_half = [&](int half) {
-#pragma unroll
-      for (int d = 2 * half; d < 2 * half + 2; ++d) {
-        raw[2 * d] = ld16(ra, d * 64 + c4 * 16);
-        raw[2 * d + 1] = ld16(rb, d * 64 + c4 * 16);
-      }
-      ex_a[half] = __ldg(reinterpret_cast<const uint2*>(ra + lat::EXP_OFF + 8 * half));
-      ex_b[half] = __ldg(reinterpret_cast<const uint2*>(rb + lat::EXP_OFF + 8 * half));
+    const uint8_t* rr;  // row of this lane's RoPE block
+    auto load_latent = [&](int32_t slots, int k) {
+      const uint8_t* r = row_ptr(slots, 2 * k + odd);
+      raw[k] = ld16(r, 16 * blk);
+      ex[k] = __ldg(r + lat::EXP_OFF + blk);
     };
     auto load_rope = [&] {
       raw_r = ld16(rr, 256 + (lane & 1) * 16);
@@ -439,9 +432,9 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     const Page g0 = find_page(t0), g1 = find_page(t1);
     Page g2 = find_page(t2);  // of tile i + 2
     int32_t slot = find_slot(g0), slot_next;
-    rows_of(slot);
-    load_half(0);
-    load_half(1);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) load_latent(slot, k);
+    rr = row_ptr(slot, lane >> 1);
     load_rope();
     slot_next = find_slot(g1);
     int32_t row = g_begin / tpr, row_left = tpr - g_begin % tpr;
@@ -451,25 +444,23 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       ring.next();
     };
     if (n > 0) skip_query();
-    const uint32_t sa = sw128_off(16 * dw + r4, 2 * c4), sb = sa ^ 16u;  // the two 16-byte halves of a block
+    // where block blk of key 16 dw + odd goes in the 128-byte swizzle; of keys further on: 256 k bytes further, chunks ^ 2 k
+    const uint32_t at0 = (blk >> 2) * SUB + sw128_off(16 * dw + odd, 2 * (blk & 3));
     for (int32_t i = 0; i < n; ++i) {
       const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0) & 0xFFFFu;
-      rows_of(slot_next);
+      rr = row_ptr(slot_next, lane >> 1);
       wait(B_EMPTY + ring.slot, ring.phase ^ 1);
       if (lane == 0) masks[(i & 3) * 8 + dw] = static_cast<uint16_t>(live);
       uint8_t* const dst = smem + OFF_KV + 4 * ring.slot * SUB;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
+      for (int k = 0; k < 8; ++k) {
         uint4 o0, o1;
-        pin(raw[2 * d]), pin(raw[2 * d + 1]);
-        const uint32_t xa = d & 1 ? ex_a[d >> 1].y : ex_a[d >> 1].x, xb = d & 1 ? ex_b[d >> 1].y : ex_b[d >> 1].x;
-        decode32(raw[2 * d], __byte_perm(xa, 0, 0x4440u | c4), o0, o1);
-        *reinterpret_cast<uint4*>(dst + d * SUB + sa) = o0;
-        *reinterpret_cast<uint4*>(dst + d * SUB + sb) = o1;
-        decode32(raw[2 * d + 1], __byte_perm(xb, 0, 0x4440u | c4), o0, o1);
-        *reinterpret_cast<uint4*>(dst + d * SUB + sa + 1024) = o0;  // 8 rows further: the same swizzle
-        *reinterpret_cast<uint4*>(dst + d * SUB + sb + 1024) = o1;
-        if (d & 1) load_half(d >> 1);  // of the next tile
+        pin(raw[k]);
+        decode32(raw[k], ex[k], o0, o1);
+        const uint32_t at = (at0 ^ (32 * (k & 3))) + 256 * k;
+        *reinterpret_cast<uint4*>(dst + at) = o0;
+        *reinterpret_cast<uint4*>(dst + (at ^ 16u)) = o1;
+        load_latent(slot_next, k);  // of the next tile
       }
       if (i >= 1) wait(B_RFREE, (i - 1) & 1);  // the one RoPE sub-tile
       {
