@@ -465,9 +465,13 @@ bool mla_query_prepass(int32_t n_q, int32_t k, int sms) {
   return cuts >= 8;
 }
 
-// The 4-bit attention's schedule: equal contiguous tile ranges over one CTA per SM.
+// The 4-bit attention's schedule over one CTA per SM.  Two shares are compared by their longest CTA: equal contiguous tile
+// ranges, which cut rows anywhere, and whole rows (or, for at most half as many rows as SMs, equal parts of one row).  A range
+// that begins inside a row costs a CTA another query and output and the call a merge, together about as much as 8 tiles
+// (at k = 2,048: 31 rows 30.8 us in ranges of 3.4 tiles, 26.7 in fourths of a row; 147 rows 73.8 and 56.8; 160 rows 78.7 in
+// ranges of 17.3 tiles, 103.7 as whole rows of which some CTAs get two; 240 rows 108.6 and 105.4; 1,024 rows 370 and 356).
 struct Plan4 {
-  int32_t tiles_per_row = 0, grid = 0;
+  int32_t tiles_per_row = 0, grid = 0, unit = 1;
   int64_t tiles = 0;
   size_t ws = 0;  // partials of the rows that range boundaries cut, 0 when none does
 };
@@ -477,7 +481,14 @@ Plan4 plan_mla4(int32_t n_q, int32_t k, int sms) {
   pl.tiles_per_row = (k + mla4::TILE - 1) / mla4::TILE;
   pl.tiles = static_cast<int64_t>(n_q) * pl.tiles_per_row;
   pl.grid = static_cast<int32_t>(std::min<int64_t>(pl.tiles, sms));
-  for (int32_t c = 1; c < pl.grid; ++c)
+  const int32_t parts = std::max(std::min(sms / n_q, pl.tiles_per_row), 1);       // of a row
+  const int32_t rows = static_cast<int32_t>((static_cast<int64_t>(n_q) + sms - 1) / sms);  // of a CTA
+  const int64_t longest = static_cast<int64_t>(rows) * ((pl.tiles_per_row + parts - 1) / parts);
+  if (longest * sms <= pl.tiles + 8LL * sms) {
+    pl.grid = parts > 1 ? n_q * parts : (n_q + rows - 1) / rows;
+    if (parts == 1) pl.unit = pl.tiles_per_row;
+  }
+  for (int32_t c = 1; c < pl.grid && pl.unit == 1; ++c)
     if ((c * pl.tiles / pl.grid) % pl.tiles_per_row) pl.ws = static_cast<size_t>(pl.grid) * 2 * (64 * 512 + 128) * 4;
   return pl;
 }
@@ -508,8 +519,9 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   p.max_pages = kv->max_pages;
   p.n_pages = static_cast<int32_t>(kv->n_tokens / DSA_PAGE);
   p.tiles_per_row = pl.tiles_per_row;
-  p.quot = static_cast<int32_t>(pl.tiles / pl.grid);
-  p.rem = static_cast<int32_t>(pl.tiles % pl.grid);
+  p.unit = pl.unit;
+  p.quot = static_cast<int32_t>(pl.tiles / pl.unit / pl.grid);
+  p.rem = static_cast<int32_t>(pl.tiles / pl.unit % pl.grid);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = ds->status;
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);

@@ -82,7 +82,8 @@ struct Params {
   float* part_o;       // [grid, 2, 16, 512, 4] fp32 (16 quads of heads, 512 dims, 4 heads)
   float* part_ml;      // [grid, 2, 2, 64] (m in log2 units, l)
   int32_t n_q, rows_per_idx, k, batch, max_pages, n_pages;
-  int32_t tiles_per_row, quot, rem;  // n_q * tiles_per_row = quot * grid + rem
+  int32_t tiles_per_row;
+  int32_t unit, quot, rem;  // ranges of whole units of tiles (1, or a row's): n_q * tiles_per_row = unit * (quot * grid + rem)
   float scale_log2;
   int* status;
   uint64_t wait_ns;
@@ -99,7 +100,7 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo) {
 // Byte offset of 16-byte chunk c (0..3) of row r inside a 64-byte-swizzled region.
 __device__ __forceinline__ uint32_t sw64_off(uint32_t r, uint32_t c) { return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4); }
 
-// First global tile of CTA c: floor(c * tiles / grid), with tiles = quot * grid + rem (no 64-bit division).
+// First unit of CTA c: floor(c * units / grid), with units = quot * grid + rem (no 64-bit division).
 __device__ __forceinline__ int32_t range_begin(int32_t c, int32_t quot, int32_t rem, int32_t grid) {
   return c * quot + c * rem / grid;
 }
@@ -293,8 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int32_t tpr = p.tiles_per_row;
-  const int32_t g_begin = range_begin(blockIdx.x, p.quot, p.rem, gridDim.x);
-  const int32_t g_end = range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
+  const int32_t g_begin = p.unit * range_begin(blockIdx.x, p.quot, p.rem, gridDim.x);
+  const int32_t g_end = p.unit * range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
   auto wait = [&](int b, uint32_t par) { wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns); };
   const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
 
