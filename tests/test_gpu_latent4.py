@@ -598,6 +598,20 @@ def test_attention_over_many_short_rows():
         check_attention(qd, kv, idx, rows, out, lse)
 
 
+@pytest.mark.parametrize("n_seqs,rows,k", [(148, 1, 260), (149, 1, 1300), (40, 4, 1100), (19, 8, 2048), (296, 1, 130)])
+def test_attention_over_all_shares_of_the_work(n_seqs, rows, k):
+    """Whole rows per SM, parts of a row, and ranges that cut rows anywhere: a sample of the rows of each."""
+    rng = np.random.default_rng(23)
+    lens = [int(n) for n in rng.integers(max(k - 40, 1), k + 300, size=n_seqs)]
+    idx = selection(rng, lens, k)
+    qd, _, kv, out, lse = run_attention(rng, lens, rows, k, idx)
+    dsa.sync_status()
+    q, o, e = f64(qd), f64(out), f64(lse)
+    for r in sorted(set([0, 1, n_seqs * rows // 2, n_seqs * rows - 1] + [int(v) for v in rng.integers(0, n_seqs * rows, 10)])):
+        ro, rl, bo, bl = reference(q[r:r + 1], kv[r // rows], idx[r // rows])
+        assert np.all(np.abs(o[r] - ro[0]) <= bo[0]) and np.all(np.abs(e[r] - rl[0]) <= bl[0]), r
+
+
 def test_two_attentions_at_once_on_streams_of_their_own():
     rng = np.random.default_rng(19)
     calls = []
