@@ -312,11 +312,13 @@ struct ReadParams {
 };
 
 // 72 threads per row, 8 values each: 4 or 8 bytes of codes in, 16 bytes of bf16 out; four rows at a time per thread, whose
-// chains of loads (position, page, codes) run side by side.  4-bit values are exact in bf16; an e4m3 code times its fp32
-// scale is rounded once.  Bound by the bytes.
+// chains of loads (position, page, codes) run side by side (two rows took as long, eight 17.1 us for 14.1).  4-bit values are
+// exact in bf16; an e4m3 code times its fp32 scale is rounded once.  Bound by the stores and the latency of the chain: 32,768
+// rows in 12.9 us, 3.7 TB/s of codes and values (14.1 us without the bound on registers, which brings seven blocks to an SM
+// instead of three).
 constexpr int READ_ROWS = 4;
 template <bool MX>
-__global__ void __launch_bounds__(288) latent_read_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(288, 7) latent_read_kernel(const __grid_constant__ ReadParams p) {
   grid_dependency_sync();
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (4 * READ_ROWS) + threadIdx.x / 72;
   const int w = threadIdx.x % 72;
