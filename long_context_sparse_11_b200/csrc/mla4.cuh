@@ -11,23 +11,26 @@
 //     floor of 2^-20 of the row's largest probability), two products into the same accumulator.
 //   S[q part, key]  = Q[part, 0:576] . KV[key, 0:576]    M = 128, N = 128, K = 32: 18 steps of 64 clocks
 //   O^T[dim, head] += V^T[dim, key] . P[head, key]       M = 128 dims x 4, N = 64, K = 32, 2 parts: 32 steps of 48 clocks
-// so a tile of 128 keys takes the tensor core about 2,700 clocks.
+// so a tile of 128 keys takes the tensor core about 2,700 clocks, the second product at the rate of shared memory (6 KB per
+// step).  A tile in fact takes about 4,000 (32 x 5 rows of 2,048 keys: 58 us alone, 69.5 us with the merge; 512 rows: 155 and
+// 180 us, 809 TFLOP/s of the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the
+// products read, and the instructions of decode and softmax share the SM with it (issue slots 51% busy, the L1 data pipe 61%).
 //
-// What bounds it is the chain of one tile (rows, decode, S, softmax, PV), which is several times that long, so three
-// tiles are in flight: a decoded tile is 64 KB (plus 8 KB of RoPE dims, one buffer), and the query row, which would take
-// that much again, stays in tensor memory as the A operand of S.  It passes through a tile's slot of the ring on its way
-// there.  Tensor memory: O^T in columns 0..255, S in 256..383, Q (512 dims) in 384..511; Q's RoPE dims in shared memory.
+// The chain of one tile (rows, decode, S, softmax, PV) is several times that long, so three tiles are in flight: a decoded tile
+// is 64 KB (plus 8 KB of RoPE dims, one buffer), and the query row, which would take that much again, stays in tensor memory as
+// the A operand of S.  It passes through a tile's slot of the ring on its way there.  Tensor memory: O^T in columns 0..255, S in
+// 256..383, Q (512 dims) in 384..511; Q's RoPE dims in shared memory.
 //
 // Warps 0..15: query rows, softmax and output (warp w: heads 16 (w % 4) .. + 15, keys 32 (w / 4) .. + 31; a lane holds 16
 // keys of one head); 8 decode warps: the next tile's 320-byte rows loaded into registers while one is decoded; 2 warps
-// issue the MMAs.  CTAs are persistent over equal contiguous ranges of the (row, key tile) sequence; rows that a
-// range boundary cuts leave fp32 partials for combine4_kernel.
+// issue the MMAs.  CTAs are persistent over contiguous ranges of the (row, key tile) sequence; rows that a range boundary cuts
+// leave fp32 partials for combine4_kernel.  A change of rows costs about 12,000 clocks (the next query's two parts, the
+// output), which is why the launch cuts rows only where that is the shorter way.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include "latent4.cuh"
-#include "mla.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -489,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   } else if (warp >= MMA_WARP) {
     // ================================================================= MMA issuer
     regs_dec<REGS_MMA>();
-    // Two warps, so that neither product waits behind the other's inputs: S^T of a tile as its halves are decoded, PV as
-    // its probabilities arrive (S^T runs up to two tiles ahead).  A whole warp runs each loop and one elected lane issues:
+    // Two warps, so that neither product waits behind the other's inputs: S of a tile once it is decoded, PV as its
+    // probabilities arrive (S runs a tile ahead).  A whole warp runs each loop and one elected lane issues:
     // every address stays in uniform registers, and an MMA costs one instruction.  (Issued by one lane of a divergent branch
     // they took 75 to 120 clocks each; one warp that polled for both streams left the tensor core idle between steps.)
     const uint32_t lo0 = (base >> 4) | (1u << 16);
@@ -767,7 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
 // Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block of 128 threads per 4
 // heads of a cut row (DIMS = 4: 4 dims of 4 heads per thread), or per 4 heads and 128 dims (DIMS = 1) when the rows are few
 // and cut into many fragments (at most 16: k <= 2,048).  One warp forms the weights while the first EARLY fragments are on
-// their way to everyone.  blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first
+// their way to everyone.  Bound by the latency of its loads: 7.1 us alone and from cold caches for 6 rows of 16 fragments
+// (12.6 MB), 9.2 us for 147 rows of two.  blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first
 // inside a row does it).
 constexpr int COMBINE_THREADS = 128;
 template <int DIMS, int EARLY>

@@ -110,8 +110,8 @@ union Pack {
 
 // One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared memory; then
 // each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (16-bit types: 2;
-// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes; each value is
-// rounded once.
+// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Each value is rounded once.  Bound by the tensor's
+// bytes: 8,192 tokens x 64 heads x 64 dims in bf16 25.8 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p,
                                                        const __grid_constant__ Freqs fr) {
