@@ -465,31 +465,28 @@ bool mla_query_prepass(int32_t n_q, int32_t k, int sms) {
   return cuts >= 8;
 }
 
-// The 4-bit attention's schedule over one CTA per SM.  Two shares are compared by their longest CTA: equal contiguous tile
-// ranges, which cut rows anywhere, and whole rows (or, for at most half as many rows as SMs, equal parts of one row).  A range
-// that begins inside a row costs a CTA another query and output and the call a merge, together about as much as 8 tiles
-// (at k = 2,048: 31 rows 30.8 us in ranges of 3.4 tiles, 26.7 in fourths of a row; 147 rows 73.8 and 56.8; 160 rows 78.7 in
-// ranges of 17.3 tiles, 103.7 as whole rows of which some CTAs get two; 240 rows 108.6 and 105.4; 1,024 rows 370 and 356).
+// The 4-bit attention's schedule, one CTA per SM: the same number of whole rows for each, and the rows that remain (fewer than
+// SMs) in as many equal parts as there are SMs for, one to a CTA.  (Equal contiguous ranges of all tiles cut more rows, and a
+// cut costs a CTA another query and output and the call its merge, together about as much as 8 tiles: at k = 2,048, with the
+// merge, 31 rows 30.8 us in ranges and 26.7 in parts, 160 rows 73.2 and 68.1, 220 rows 97.0 and 86.6, 512 rows 193.5 and
+// 185.7, 1,024 rows 370 and 349.)  Parts that shorten a row by fewer than 3 tiles are not worth the merge: 330 rows of 256 keys
+// 37.9 us in parts of one tile, 34.9 whole.
 struct Plan4 {
-  int32_t tiles_per_row = 0, grid = 0, unit = 1;
+  int32_t tiles_per_row = 0, grid = 0, whole_rows = 0, cut_rows = 0, parts = 1;
   int64_t tiles = 0;
-  size_t ws = 0;  // partials of the rows that range boundaries cut, 0 when none does
+  size_t ws = 0;  // partials of the cut rows
 };
 Plan4 plan_mla4(int32_t n_q, int32_t k, int sms) {
   Plan4 pl;
   if (n_q <= 0 || k <= 0) return pl;
   pl.tiles_per_row = (k + mla4::TILE - 1) / mla4::TILE;
   pl.tiles = static_cast<int64_t>(n_q) * pl.tiles_per_row;
-  pl.grid = static_cast<int32_t>(std::min<int64_t>(pl.tiles, sms));
-  const int32_t parts = std::max(std::min(sms / n_q, pl.tiles_per_row), 1);       // of a row
-  const int32_t rows = static_cast<int32_t>((static_cast<int64_t>(n_q) + sms - 1) / sms);  // of a CTA
-  const int64_t longest = static_cast<int64_t>(rows) * ((pl.tiles_per_row + parts - 1) / parts);
-  if (longest * sms <= pl.tiles + 8LL * sms) {
-    pl.grid = parts > 1 ? n_q * parts : (n_q + rows - 1) / rows;
-    if (parts == 1) pl.unit = pl.tiles_per_row;
-  }
-  for (int32_t c = 1; c < pl.grid && pl.unit == 1; ++c)
-    if ((c * pl.tiles / pl.grid) % pl.tiles_per_row) pl.ws = static_cast<size_t>(pl.grid) * 2 * (64 * 512 + 128) * 4;
+  pl.whole_rows = n_q / sms;
+  pl.cut_rows = n_q % sms;
+  if (pl.cut_rows) pl.parts = std::min(sms / pl.cut_rows, pl.tiles_per_row);
+  if (pl.tiles_per_row - (pl.tiles_per_row + pl.parts - 1) / pl.parts < 3) pl.parts = 1;
+  pl.grid = pl.whole_rows ? sms : pl.cut_rows * pl.parts;
+  if (pl.parts > 1) pl.ws = static_cast<size_t>(pl.cut_rows) * pl.parts * (64 * 512 + 128) * 4;
   return pl;
 }
 
@@ -511,7 +508,7 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = static_cast<float*>(ws);
-  p.part_ml = p.part_o + static_cast<size_t>(pl.grid) * 2 * 64 * 512;
+  p.part_ml = p.part_o + static_cast<size_t>(pl.cut_rows) * pl.parts * 64 * 512;
   p.n_q = n_q;
   p.rows_per_idx = rpi;
   p.k = k;
@@ -519,9 +516,9 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   p.max_pages = kv->max_pages;
   p.n_pages = static_cast<int32_t>(kv->n_tokens / DSA_PAGE);
   p.tiles_per_row = pl.tiles_per_row;
-  p.unit = pl.unit;
-  p.quot = static_cast<int32_t>(pl.tiles / pl.unit / pl.grid);
-  p.rem = static_cast<int32_t>(pl.tiles / pl.unit % pl.grid);
+  p.whole_rows = pl.whole_rows;
+  p.parts = pl.parts;
+  p.n_parts = pl.cut_rows * pl.parts;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.status = ds->status;
   p.wait_ns = static_cast<uint64_t>(g_wait_ns);
@@ -529,14 +526,14 @@ dsa_status launch_mla4(const void* q, const dsa_cache_view* kv, const int32_t* i
   count_launch();
   DSA_TRY(cuda_check(cudaGetLastError(), "4-bit sparse MLA launch"));
   if (pl.ws > 0) {
-    const int32_t by_row = n_q < pl.grid - 1 ? 1 : 0;
-    const unsigned cuts = static_cast<unsigned>(by_row ? n_q : pl.grid - 1);
-    if (by_row && n_q * 8 <= pl.grid)  // few rows of 8 and more fragments: more blocks, more fragments in flight
-      launch_pdl(mla4::combine4_kernel<1, 8>, dim3(cuts, 16, 4), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
-                 p.tiles_per_row, p.quot, p.rem, pl.grid, by_row, p.out, p.lse);
+    const unsigned rows = static_cast<unsigned>(pl.cut_rows);
+    const int32_t base = pl.whole_rows * pl.grid;
+    if (pl.parts >= 8)  // few rows: more blocks, more parts in flight
+      launch_pdl(mla4::combine4_kernel<1, 8>, dim3(rows, 16, 4), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
+                 pl.parts, base, p.out, p.lse);
     else
-      launch_pdl(mla4::combine4_kernel<4, 2>, dim3(cuts, 16, 1), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
-                 p.tiles_per_row, p.quot, p.rem, pl.grid, by_row, p.out, p.lse);
+      launch_pdl(mla4::combine4_kernel<4, 2>, dim3(rows, 16, 1), mla4::COMBINE_THREADS, 0, st, p.part_o, p.part_ml,
+                 pl.parts, base, p.out, p.lse);
     count_launch();
     DSA_TRY(cuda_check(cudaGetLastError(), "4-bit combine launch"));
   }

@@ -12,9 +12,9 @@
 //   S[q part, key]  = Q[part, 0:576] . KV[key, 0:576]    M = 128, N = 128, K = 32: 18 steps of 64 clocks
 //   O^T[dim, head] += V^T[dim, key] . P[head, key]       M = 128 dims x 4, N = 64, K = 32, 2 parts: 32 steps of 48 clocks
 // so a tile of 128 keys takes the tensor core about 2,700 clocks, the second product at the rate of shared memory (6 KB per
-// step).  A tile in fact takes about 4,000 (32 x 5 rows of 2,048 keys: 58 us alone, 69.5 us with the merge; 512 rows: 155 and
-// 180 us, 809 TFLOP/s of the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the
-// products read, and the instructions of decode and softmax share the SM with it (issue slots 51% busy, the L1 data pipe 61%).
+// step).  A tile in fact takes about 4,000 (32 x 5 rows of 2,048 keys 67 us with the merge; 512 rows 177 us, 824 TFLOP/s of
+// the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the products read, and the
+// instructions of decode and softmax share the SM with it (issue slots 51% busy, the L1 data pipe 61%).
 //
 // The chain of one tile (rows, decode, S, softmax, PV) is several times that long, so three tiles are in flight: a decoded tile
 // is 64 KB (plus 8 KB of RoPE dims, one buffer), and the query row, which would take that much again, stays in tensor memory as
@@ -23,9 +23,8 @@
 //
 // Warps 0..15: query rows, softmax and output (warp w: heads 16 (w % 4) .. + 15, keys 32 (w / 4) .. + 31; a lane holds 16
 // keys of one head); 8 decode warps: the next tile's 320-byte rows loaded into registers while one is decoded; 2 warps
-// issue the MMAs.  CTAs are persistent over contiguous ranges of the (row, key tile) sequence; rows that a range boundary cuts
-// leave fp32 partials for combine4_kernel.  A change of rows costs about 12,000 clocks (the next query's two parts, the
-// output), which is why the launch cuts rows only where that is the shorter way.
+// issue the MMAs.  CTAs are persistent over whole rows and, last, an equal part of a row that several CTAs share, which leaves
+// fp32 partials for combine4_kernel.  A change of rows costs about 12,000 clocks (the next query's two parts, the output).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -81,12 +80,12 @@ struct Params {
   const int32_t* idx;  // [n_q / rows_per_idx, k]
   uint16_t* out;       // [n_q, 64, 512] bf16
   float* lse;          // [n_q, 64] or null
-  // A CTA's range holds at most two cut rows: one begun before it (fragment 0), one that ends after it (fragment 1).
-  float* part_o;       // [grid, 2, 16, 512, 4] fp32 (16 quads of heads, 512 dims, 4 heads)
-  float* part_ml;      // [grid, 2, 2, 64] (m in log2 units, l)
+  float* part_o;       // [parts of rows, 16, 512, 4] fp32 (16 quads of heads, 512 dims, 4 heads)
+  float* part_ml;      // [parts of rows, 2, 64] (m in log2 units, l)
   int32_t n_q, rows_per_idx, k, batch, max_pages, n_pages;
-  int32_t tiles_per_row;
-  int32_t unit, quot, rem;  // ranges of whole units of tiles (1, or a row's): n_q * tiles_per_row = unit * (quot * grid + rem)
+  // CTA c has the whole rows whole_rows * c ..; the rows behind those of all CTAs are cut into `parts` equal parts (1: not
+  // cut), and CTA c < n_parts has part c of them.
+  int32_t tiles_per_row, whole_rows, parts, n_parts;
   float scale_log2;
   int* status;
   uint64_t wait_ns;
@@ -103,9 +102,16 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo) {
 // Byte offset of 16-byte chunk c (0..3) of row r inside a 64-byte-swizzled region.
 __device__ __forceinline__ uint32_t sw64_off(uint32_t r, uint32_t c) { return r * 64u + ((c ^ ((r >> 1) & 3u)) << 4); }
 
-// First unit of CTA c: floor(c * units / grid), with units = quot * grid + rem (no 64-bit division).
-__device__ __forceinline__ int32_t range_begin(int32_t c, int32_t quot, int32_t rem, int32_t grid) {
-  return c * quot + c * rem / grid;
+// Row k of a CTA in its order: its whole rows, then its part of a cut row (which ends with the CTA's tiles).  Worked out anew
+// at each row's end: more of it kept in registers, and the softmax warps spill.
+struct Row {
+  int32_t row, first;  // first: its first tile
+};
+__device__ __forceinline__ Row row_of(const Params& p, int32_t k) {
+  const int32_t c = blockIdx.x;
+  if (k < p.whole_rows) return Row{p.whole_rows * c + k, 0};
+  const int32_t r = c / p.parts, s = c - r * p.parts;
+  return Row{p.whole_rows * static_cast<int32_t>(gridDim.x) + r, s * p.tiles_per_row / p.parts};
 }
 
 // Keeps the arithmetic on loaded registers behind this point (moved up, it would wait for loads just issued).
@@ -297,10 +303,13 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int32_t tpr = p.tiles_per_row;
-  const int32_t g_begin = p.unit * range_begin(blockIdx.x, p.quot, p.rem, gridDim.x);
-  const int32_t g_end = p.unit * range_begin(blockIdx.x + 1, p.quot, p.rem, gridDim.x);
   auto wait = [&](int b, uint32_t par) { wait_phase(bar(b), par, abort_flag, p.status, p.wait_ns); };
-  const int32_t n = g_end - g_begin;  // this CTA's tiles; below, tile i is global tile g_begin + i
+  int32_t n = p.whole_rows * tpr;  // this CTA's tiles
+  if (blockIdx.x < p.n_parts) {
+    const int32_t s = blockIdx.x % p.parts;
+    n += (s + 1) * tpr / p.parts - s * tpr / p.parts;
+  }
+  const Row row0 = row_of(p, 0);
 
   // The ring's slots in the order of their use: a row's query, then its tiles.  On a fresh barrier the wait for the phase
   // before the first passes.
@@ -377,12 +386,12 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       int32_t t, page;
     };
     struct {
-      int32_t left, at, row, irow;
+      int32_t left, at, item, irow;
     } ahead;
     ahead.left = n;
-    ahead.row = g_begin / tpr;
-    ahead.irow = ahead.row / p.rows_per_idx;
-    ahead.at = g_begin % tpr * TILE + 16 * dw + lane;
+    ahead.item = 0;
+    ahead.irow = row0.row / p.rows_per_idx;
+    ahead.at = row0.first * TILE + 16 * dw + lane;
     auto position = [&]() -> Pos {
       const bool in = ahead.left > 0;
       const Pos q{load_if(in && lane < 16 && ahead.at < p.k, p.idx + static_cast<int64_t>(ahead.irow) * p.k + ahead.at),
@@ -390,8 +399,9 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       --ahead.left;
       ahead.at += TILE;
       if (ahead.at >= tpr * TILE) {
-        ahead.at = 16 * dw + lane;
-        ahead.irow = ++ahead.row / p.rows_per_idx;
+        const Row next = row_of(p, ++ahead.item);
+        ahead.irow = next.row / p.rows_per_idx;
+        ahead.at = next.first * TILE + 16 * dw + lane;
       }
       return q;
     };
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     rr = row_ptr(slot, lane >> 1);
     load_rope();
     slot_next = find_slot(g1);
-    int32_t row = g_begin / tpr, row_left = tpr - g_begin % tpr;
+    int32_t item = 0, row_left = tpr - row0.first;
     // A row's query is the softmax warps' work: here its use of a slot only keeps the barriers' phases in step.
     auto skip_query = [&] {
       if (lane == 0) mbar_arrive(bar(B_FULL + ring.slot));
@@ -482,10 +492,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       slot_next = find_slot(g2);
       g2 = find_page(t3);
       t3 = position();
-      if (row_left == 3 && i + 3 < n) q_prefetch(row + 1);
+      if (row_left == 3 && i + 3 < n) q_prefetch(row_of(p, item + 1).row);
       if (--row_left == 0) {
-        row_left = tpr;
-        ++row;
+        row_left = tpr;  // (a part's tiles end with n)
+        ++item;
         if (i + 1 < n) skip_query();
       }
     }
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
           }
           __syncwarp();
           ring.next();
-          row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+          row_left = i == 0 ? tpr - row0.first : tpr;
         }
         --row_left;
         if (i > 0) wait(B_SREAD, (i - 1) & 1);
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       for (int32_t i = 0; i < n; ++i) {
         const uint32_t keep = row_left == 0 ? 0u : 1u;  // a row's first tile starts its sum
         if (row_left == 0) {
-          row_left = i == 0 ? tpr - g_begin % tpr : tpr;
+          row_left = i == 0 ? tpr - row0.first : tpr;
           ring.next();  // past the row's query
         }
         --row_left;
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     Ring ring;
     if (n > 0) {
       uint2 hi, lo;
-      q_stage(g_begin / tpr, 0, 0, 4 * warp, hi, lo);
+      q_stage(row0.row, 0, 0, 4 * warp, hi, lo);
       q_stage_rope(4 * warp, hi, lo);
       fence_async_smem();
       __syncwarp();
@@ -589,20 +599,14 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     uint32_t one;
     asm volatile("mov.b32 %0, 1;" : "=r"(one));
     int32_t item = 0;
-    float z = 0.f, nn = 0.f;  // logit scale, BIAS minus the running maximum
+    float z = 0.f, nn = BIAS;  // logit scale, BIAS minus the running maximum
     uint64_t lsum = 0ull;     // two partial row sums
     bool seen = false;        // the item has had a key that counts (its maxima are set)
-    int32_t row = g_begin / tpr, j = g_begin % tpr;
+    int32_t left = min(tpr - row0.first, n);  // left: tiles of the row still to come
     for (int32_t i = 0; i < n; ++i) {
-      const bool last = i == n - 1 || j == tpr - 1;
       wait(B_SFULL, i & 1);
       tc_fence_after();
-      if (i == 0 || j == 0) {
-        z = zs[(item & 3) * 64 + head];
-        nn = BIAS;
-        lsum = 0ull;
-        seen = false;
-      }
+      if (!seen) z = zs[(item & 3) * 64 + head];
       const uint32_t mine = *reinterpret_cast<const uint32_t*>(misc + M_MASK + (i & 3) * 16 + grp * 4);
       uint64_t t[8];  // log2 of p / 256 of keys 2 u, 2 u + 1
       {
@@ -688,13 +692,12 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PFULL));
-      ++j;
       ring.next();
-      if (!last) continue;
+      if (--left > 0) continue;
       if (i + 1 < n) {  // the next row's query, while the last PV runs (S has read the present one)
         wait(B_EMPTY + ring.slot, ring.phase ^ 1);
         uint2 hi, lo;
-        q_stage(row + 1, item + 1, ring.slot, 4 * warp, hi, lo);
+        q_stage(row_of(p, item + 1).row, item + 1, ring.slot, 4 * warp, hi, lo);
         q_stage_rope(4 * warp, hi, lo);
         fence_async_smem();
         __syncwarp();
@@ -702,16 +705,15 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
         ring.next();
       }
       // ---- end of item: wait for its last PV, reduce the row sums, write the output
-      ++item;
+      const int32_t row = row_of(p, item++).row;
       float l = unpack2(lsum).x + unpack2(lsum).y;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       wait(B_PVDONE, i & 1);  // every warp has written P, so none still reads its tile's maxima in red
       tc_fence_after();
       if (upper == 0) red[grp * 64 + head] = l;
       named_bar(1, SM_THREADS);
-      const int32_t row0 = row * tpr;  // this row's first global tile
-      const bool whole = row0 >= g_begin && row0 + tpr <= g_end;
-      const int64_t pr = static_cast<int64_t>(blockIdx.x) * 2 + (row0 >= g_begin ? 1 : 0);
+      const bool whole = p.parts == 1 || row < p.whole_rows * static_cast<int32_t>(gridDim.x);
+      const int64_t pr = blockIdx.x;
       if (grp == 0 && upper == 0) {
         l = 256.f * (red[head] + red[64 + head] + red[128 + head] + red[192 + head]);  // sum of p
         alpha[head] = l == 0.f ? 0.f : 1.f / l;
@@ -755,8 +757,10 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
                 make_float4(__uint_as_float(x[c]), __uint_as_float(x[c + 1]), __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
         }
       }
-      ++row;
-      j = 0;
+      left = min(tpr, n - 1 - i);
+      nn = BIAS;
+      lsum = 0ull;
+      seen = false;
       tc_fence_before();
       named_bar(1, SM_THREADS);  // alpha and red are the next item's
     }
@@ -767,37 +771,21 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
   if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Rows cut over several CTAs: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block of 128 threads per 4
-// heads of a cut row (DIMS = 4: 4 dims of 4 heads per thread), or per 4 heads and 128 dims (DIMS = 1) when the rows are few
-// and cut into many fragments (at most 16: k <= 2,048).  One warp forms the weights while the first EARLY fragments are on
-// their way to everyone.  Bound by the latency of its loads: 7.1 us alone and from cold caches for 6 rows of 16 fragments
-// (12.6 MB), 9.2 us for 147 rows of two.  blockIdx.x is a row when there are fewer rows than range boundaries, else a boundary (the first
-// inside a row does it).
+// Cut rows: out = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).  One block of 128 threads per 4 heads of a cut row
+// (DIMS = 4: 4 dims of 4 heads per thread), or per 4 heads and 128 dims (DIMS = 1) when the rows are few and cut into many
+// parts (at most 16: k <= 2,048).  One warp forms the weights while the first EARLY parts are on their way to everyone.
+// Bound by the latency of its loads: 7.1 us alone and from cold caches for 6 rows of 16 parts (12.6 MB).
 constexpr int COMBINE_THREADS = 128;
 template <int DIMS, int EARLY>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* __restrict__ part_o,
-                                                                   const float* __restrict__ part_ml, int32_t tpr,
-                                                                   int32_t quot, int32_t rem, int32_t grid, int32_t by_row,
-                                                                   uint16_t* __restrict__ out, float* __restrict__ lse) {
+                                                                   const float* __restrict__ part_ml, int32_t n,
+                                                                   int32_t base, uint16_t* __restrict__ out,
+                                                                   float* __restrict__ lse) {
   grid_dependency_sync();
   __shared__ float wgt[16][4], inv[4];
   const int32_t hq = blockIdx.y, dim = (DIMS == 1 ? blockIdx.z * COMBINE_THREADS : 0) + threadIdx.x;
-  int32_t row, c;  // the row's first fragment is CTA c - 1's
-  if (by_row) {
-    row = blockIdx.x;
-    // the first boundary past the row's first tile
-    c = row * tpr * grid / (quot * grid + rem);
-    while (c < grid && range_begin(c, quot, rem, grid) <= row * tpr) ++c;
-    if (c >= grid || range_begin(c, quot, rem, grid) >= (row + 1) * tpr) return;
-  } else {
-    c = blockIdx.x + 1;
-    const int32_t b = range_begin(c, quot, rem, grid);
-    row = b / tpr;
-    if (b % tpr == 0 || range_begin(c - 1, quot, rem, grid) > row * tpr) return;
-  }
-  int32_t n = 2;  // CTA c - 1 (its fragment 1), then CTAs c, c + 1, ... (their fragment 0)
-  while (c + n - 1 < grid && range_begin(c + n - 1, quot, rem, grid) < (row + 1) * tpr) ++n;
-  auto frag = [&](int s) { return (c - 1 + s) * 2 + (s == 0 ? 1 : 0); };
+  const int32_t row = base + blockIdx.x;  // the cut rows' parts, n each, follow one another
+  auto frag = [&](int s) { return static_cast<int32_t>(blockIdx.x) * n + s; };
   float4 o[EARLY][DIMS];
   auto fetch = [&](int s0) {
 #pragma unroll
