@@ -1230,13 +1230,12 @@ dsa_status dsa_latent_read(const dsa_cache_view* cache, const int32_t* seq, cons
   p.batch = cache->batch;
   p.max_pages = cache->max_pages;
   p.n_pages = static_cast<int32_t>(cache->n_tokens / DSA_PAGE);
-  const int64_t rows = 4 * lat::READ_ROWS;  // per CTA
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + rows - 1) / rows);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(n_rows) + lat::READ_ROWS - 1) / lat::READ_ROWS);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cache->dtype == DSA_MXFP4)
-    launch_pdl(lat::latent_read_kernel<true>, grid, 288, 0, st, p);
+    launch_pdl(lat::latent_read_kernel<true>, grid, lat::READ_THREADS, 0, st, p);
   else
-    launch_pdl(lat::latent_read_kernel<false>, grid, 288, 0, st, p);
+    launch_pdl(lat::latent_read_kernel<false>, grid, lat::READ_THREADS, 0, st, p);
   count_launch();
   return cuda_check(cudaGetLastError(), "latent read launch");
 }

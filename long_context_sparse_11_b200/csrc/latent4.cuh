@@ -314,73 +314,63 @@ struct ReadParams {
   int32_t n_rows, batch, max_pages, n_pages;
 };
 
-// 72 threads per row, 8 values each: 4 or 8 bytes of codes in, 16 bytes of bf16 out; four rows at a time per thread, whose
-// chains of loads (position, page, codes) run side by side (two rows took as long, eight 17.1 us for 14.1).  4-bit values are
-// exact in bf16; an e4m3 code times its fp32 scale is rounded once.  Bound by the stores and the latency of the chain: 32,768
-// rows in 12.9 us, 3.7 TB/s of codes and values (14.1 us without the bound on registers, which brings seven blocks to an SM
-// instead of three).
-constexpr int READ_ROWS = 4;
+// 12 threads per row, thread w with words w, w + 12, .. of 8 values (4 or 8 bytes of codes in, 16 bytes of bf16 out): the
+// loads of a row are in flight together behind its chain of position and page, and neighbouring threads store neighbouring
+// bytes.  4-bit values are exact in bf16; an e4m3 code times its fp32 scale is rounded once.  Bound by that chain and the
+// stores: 32,768 4-bit rows in 11.0 us, 4.4 TB/s of codes and values (a thread per word, four rows each, spent 73% of the
+// issue slots mostly on addresses and took 12.9).
+constexpr int READ_LANES = 12, READ_WORDS = 6, READ_THREADS = 288;
+constexpr int READ_ROWS = READ_THREADS / READ_LANES;
 template <bool MX>
-__global__ void __launch_bounds__(288, 7) latent_read_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(READ_THREADS, 7) latent_read_kernel(const __grid_constant__ ReadParams p) {
   grid_dependency_sync();
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (4 * READ_ROWS) + threadIdx.x / 72;
-  const int w = threadIdx.x % 72;
-  int32_t b[READ_ROWS], t[READ_ROWS];
-  int64_t slot[READ_ROWS];
-#pragma unroll
-  for (int k = 0; k < READ_ROWS; ++k) {
-    const int64_t r = r0 + 4 * k;
-    const bool in = r < p.n_rows;
-    b[k] = in && p.seq ? p.seq[r] : static_cast<int32_t>(r);
-    t[k] = in ? p.pos[r] : -1;
+  const int32_t g = threadIdx.x / READ_LANES, w = threadIdx.x - g * READ_LANES;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * READ_ROWS + g;
+  if (r >= p.n_rows) return;
+  const int32_t b = p.seq ? p.seq[r] : static_cast<int32_t>(r), t = p.pos[r];
+  const int64_t slot = slot_of(b, t, p.block_table, p.batch, p.max_pages, p.n_pages);
+  if (slot < 0 || t >= p.seq_lens[b]) {
+    if (w == 0) atomicOr(p.status, DEVERR_BOUNDS);
+    return;
   }
+  const uint8_t* row = p.pool + slot * (MX ? ROW4 : DIM);
+  uint2 codes[READ_WORDS];
+  uint32_t ex[READ_WORDS];
+  float scale = 1.f;
 #pragma unroll
-  for (int k = 0; k < READ_ROWS; ++k) {
-    slot[k] = -1;
-    if (r0 + 4 * k >= p.n_rows) continue;
-    slot[k] = slot_of(b[k], t[k], p.block_table, p.batch, p.max_pages, p.n_pages);
-    if (slot[k] >= 0 && t[k] >= p.seq_lens[b[k]]) slot[k] = -1;
-    if (slot[k] < 0 && w == 0) atomicOr(p.status, DEVERR_BOUNDS);
-  }
-  uint2 codes[READ_ROWS];
-  float scale[READ_ROWS];
-  uint32_t ex[READ_ROWS];
-#pragma unroll
-  for (int k = 0; k < READ_ROWS; ++k) {
-    if (slot[k] < 0) continue;
+  for (int u = 0; u < READ_WORDS; ++u) {
     if (MX) {
-      const uint8_t* row = p.pool + slot[k] * ROW4;
-      codes[k].x = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * w));
-      ex[k] = __ldg(row + EXP_OFF + w / 4);
+      codes[u].x = __ldg(reinterpret_cast<const uint32_t*>(row + 4 * w + 4 * READ_LANES * u));
+      ex[u] = __ldg(row + EXP_OFF + w / 4 + READ_LANES / 4 * u);
     } else {
-      codes[k] = __ldg(reinterpret_cast<const uint2*>(p.pool + slot[k] * DIM + 8 * w));
-      scale[k] = __ldg(p.scale + slot[k]);
+      codes[u] = __ldg(reinterpret_cast<const uint2*>(row + 8 * w + 8 * READ_LANES * u));
     }
   }
+  if (!MX) scale = __ldg(p.scale + slot);
+  uint16_t* out = p.out + r * p.out_stride + 8 * w;
 #pragma unroll
-  for (int k = 0; k < READ_ROWS; ++k) {
-    if (slot[k] < 0) continue;
+  for (int u = 0; u < READ_WORDS; ++u) {
     uint32_t o[4];
     if (MX) {
-      const uint2 m = word_to_e5m2(codes[k].x, mag_table(ex[k]));
+      const uint2 m = word_to_e5m2(codes[u].x, mag_table(ex[u]));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // an e5m2 byte is the high byte of the f16 of the same value
         const uint32_t h2 = __byte_perm(0u, i < 2 ? m.x : m.y, i & 1 ? 0x7060 : 0x5040);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&r);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+        o[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t c2 = ((i < 2 ? codes[k].x : codes[k].y) >> (16 * (i & 1))) & 0xFFFFu;
+        const uint32_t c2 = ((i < 2 ? codes[u].x : codes[u].y) >> (16 * (i & 1))) & 0xFFFFu;
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c2), __NV_E4M3);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(__half2float(__ushort_as_half(h.x)) * scale[k],
-                                                       __half2float(__ushort_as_half(h.y)) * scale[k]);
-        o[i] = *reinterpret_cast<const uint32_t*>(&r);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(__half2float(__ushort_as_half(h.x)) * scale,
+                                                       __half2float(__ushort_as_half(h.y)) * scale);
+        o[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
     }
-    *reinterpret_cast<uint4*>(p.out + (r0 + 4 * k) * p.out_stride + 8 * w) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(out + 8 * READ_LANES * u) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
