@@ -14,7 +14,7 @@
 // so a tile of 128 keys takes the tensor core about 2,700 clocks, the second product at the rate of shared memory (6 KB per
 // step).  A tile in fact takes about 4,000 (32 x 5 rows of 2,048 keys 67 us with the merge; 512 rows 177 us, 824 TFLOP/s of
 // the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the products read, and the
-// instructions of decode and softmax share the SM with it (issue slots 51% busy, the L1 data pipe 61%).
+// instructions of decode and softmax share the SM with it (512 rows: issue slots 56% busy, the L1 data pipe 59%).
 //
 // The chain of one tile (rows, decode, S, softmax, PV) is several times that long, so three tiles are in flight: a decoded tile
 // is 64 KB (plus 8 KB of RoPE dims, one buffer), and the query row, which would take that much again, stays in tensor memory as
