@@ -332,7 +332,8 @@ def topk_no_alloc(scores, k: int, out, row_len=None, causal_len0: int = 0, max_l
 
 
 def sparse_mla_workspace_bytes(n_q: int, k: int, kv: CacheView) -> int:
-    """Bytes of device workspace that :func:`sparse_mla_attn` needs for these sizes (0: none)."""
+    """Bytes of device workspace that :func:`sparse_mla_attn` needs for these sizes (0: none).  Calls that may run at the
+    same time, replayed graphs among them, need one each."""
     return load().dsa_sparse_mla_workspace_bytes(n_q, k, ctypes.byref(kv))
 
 
