@@ -452,8 +452,11 @@ __global__ void __launch_bounds__(THREADS, 1) sparse_mla4_kernel(const __grid_co
     load_rope();
     slot_next = find_slot(g1);
     int32_t item = 0, row_left = tpr - row0.first;
-    // A row's query is the softmax warps' work: here its use of a slot only keeps the barriers' phases in step.
+    // A row's query is the softmax warps' work: here its use of a slot only keeps the barriers' phases in step.  The wait
+    // belongs to that: a slot's release is one bit of its phase, and a warp that left one out would, with rows of one tile,
+    // take the tile's slot while PV of the tile two uses before still reads it.
     auto skip_query = [&] {
+      wait(B_EMPTY + ring.slot, ring.phase ^ 1);
       if (lane == 0) mbar_arrive(bar(B_FULL + ring.slot));
       ring.next();
     };
