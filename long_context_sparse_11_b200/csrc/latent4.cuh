@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
   }
   const int da = p.half ? NOPE + lane : NOPE + 2 * lane, db = p.half ? NOPE + 32 + lane : NOPE + 2 * lane + 1;
   float ra = load1(row, da, F32), rb = load1(row, db, F32);
-  float g[2][8];
+  __align__(16) float g[2][8];
   if (p.gamma) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

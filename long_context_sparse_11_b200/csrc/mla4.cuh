@@ -785,7 +785,8 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine4_kernel(const float* 
                                                                    int32_t base, uint16_t* __restrict__ out,
                                                                    float* __restrict__ lse) {
   grid_dependency_sync();
-  __shared__ float wgt[16][4], inv[4];
+  __shared__ __align__(16) float wgt[16][4];  // a fragment's weights are read at once
+  __shared__ float inv[4];
   const int32_t hq = blockIdx.y, dim = (DIMS == 1 ? blockIdx.z * COMBINE_THREADS : 0) + threadIdx.x;
   const int32_t row = base + blockIdx.x;  // the cut rows' parts, n each, follow one another
   auto frag = [&](int s) { return static_cast<int32_t>(blockIdx.x) * n + s; };
