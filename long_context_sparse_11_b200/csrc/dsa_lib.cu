@@ -1124,11 +1124,13 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t
   const int64_t total = per_head * n_heads * n_tokens;
   const int64_t want = std::min<int64_t>(std::max<int64_t>(total / (4LL * ds->sms), rope::THREADS), 8 * rope::THREADS);
   const int64_t per_tok = per_head * n_heads;
+  const int64_t pair_bytes = dtype == DSA_F32 ? sizeof(double2) : sizeof(float2);
+  const int64_t most = std::min<int64_t>(32, 32768 / (pair_bytes * (p.rot / 2)));  // tokens whose pairs fill 32 KB
   if (per_tok >= want) {
     p.tok_per_cta = 1;
     p.head_per_cta = static_cast<int32_t>(std::min<int64_t>(n_heads, (want + per_head - 1) / per_head));
   } else {
-    p.tok_per_cta = static_cast<int32_t>(std::min<int64_t>(32, (want + per_tok - 1) / per_tok));
+    p.tok_per_cta = static_cast<int32_t>(std::min<int64_t>(most, (want + per_tok - 1) / per_tok));
     p.head_per_cta = n_heads;
   }
   p.head_groups = (n_heads + p.head_per_cta - 1) / p.head_per_cta;
@@ -1138,7 +1140,7 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t
   p.by_heads = rope::make_div(static_cast<uint32_t>(p.head_per_cta));
   const int64_t grid = (static_cast<int64_t>(n_tokens) + p.tok_per_cta - 1) / p.tok_per_cta * p.head_groups;
   if (grid > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many tokens x heads");
-  const size_t smem = static_cast<size_t>(p.tok_per_cta) * (p.rot / 2) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(p.tok_per_cta) * (p.rot / 2) * pair_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 g(static_cast<unsigned>(grid));
   if (dtype == DSA_BF16)

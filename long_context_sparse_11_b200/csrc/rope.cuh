@@ -1,7 +1,7 @@
 // Rotary positions (dsa_rope) and the angle arithmetic that the cache append shares.
 //
 // Pair i of the rotated dims turns by a = pos * inv_freq[i]; both are held in double and the angle is
-// reduced to [-pi, pi] before its sine and cosine, so positions of 10^6 and more lose nothing (an fp32
+// reduced to [-pi/4, pi/4] before its sine and cosine, so positions of 10^6 and more lose nothing (an fp32
 // angle of 10^6 radians is off by 0.03).
 #pragma once
 #include <cuda_bf16.h>
@@ -85,6 +85,19 @@ struct Vec {
   static constexpr int N = 16 / static_cast<int>(sizeof(T));
 };
 
+// A pair's cosine and sine, scaled.  16-bit types turn in fp32: three roundings of 2^-24 of |a| + |b| before the one to T,
+// which is 2^13 times as coarse and more.  fp32 turns in double, so that its one rounding is the result's.
+template <typename T>
+struct Turn {
+  using Real = float;
+  using Pair = float2;
+};
+template <>
+struct Turn<float> {
+  using Real = double;
+  using Pair = double2;
+};
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
 template <>
@@ -110,13 +123,16 @@ union Pack {
 
 // One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared memory; then
 // each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (16-bit types: 2;
-// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Each value is rounded once.  Bound by the tensor's
-// bytes: 8,192 tokens x 64 heads x 64 dims in bf16 25.8 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.
+// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes: 8,192 tokens x 64
+// heads x 64 dims in bf16 25.8 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p,
                                                        const __grid_constant__ Freqs fr) {
   grid_dependency_sync();
-  extern __shared__ float2 cs[];  // [tok_per_cta][rot / 2] (cos, sin), scaled
+  using Real = typename Turn<T>::Real;
+  using Pair = typename Turn<T>::Pair;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  Pair* cs = reinterpret_cast<Pair*>(rope_smem);  // [tok_per_cta][rot / 2]
   constexpr int V = Vec<T>::N, UNROLL = sizeof(T) == 2 ? 2 : 4;
   const int32_t tg = static_cast<int32_t>(quotient(blockIdx.x, p.by_groups));
   const int32_t t0 = tg * p.tok_per_cta;
@@ -127,7 +143,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
     const int32_t t = static_cast<int32_t>(quotient(i, p.by_pairs));
     double s, c;
     sin_cos(p.pos[t0 + t], fr.f[i - t * pairs], s, c);
-    cs[i] = make_float2(static_cast<float>(c * p.mscale), static_cast<float>(s * p.mscale * p.sin_sign));
+    cs[i] = Pair{static_cast<Real>(c * p.mscale), static_cast<Real>(s * p.mscale * p.sin_sign)};
   }
   __syncthreads();
   const int32_t turn_units = p.half ? pairs / V : p.rot / V, units = static_cast<int32_t>(p.by_units.d);
@@ -160,23 +176,23 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
     for (int k = 0; k < UNROLL; ++k) {
       if (step[k] < 0) continue;
       if (step[k] < turn_units) {
-        const float2* ct = cs + tok[k] * pairs;
+        const Pair* ct = cs + tok[k] * pairs;
         if (p.half) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float2 w = ct[step[k] * V + j];
-            const float xa = to_f32(a[k].t[j]), xb = to_f32(b[k].t[j]);
-            a[k].t[j] = from_f32<T>(xa * w.x - xb * w.y);
-            b[k].t[j] = from_f32<T>(xa * w.y + xb * w.x);
+            const Pair w = ct[step[k] * V + j];
+            const Real xa = to_f32(a[k].t[j]), xb = to_f32(b[k].t[j]);
+            a[k].t[j] = from_f32<T>(static_cast<float>(xa * w.x - xb * w.y));
+            b[k].t[j] = from_f32<T>(static_cast<float>(xa * w.y + xb * w.x));
           }
           *reinterpret_cast<uint4*>(dst[k] + pairs) = b[k].u;
         } else {
 #pragma unroll
           for (int j = 0; j < V; j += 2) {
-            const float2 w = ct[(step[k] * V + j) / 2];
-            const float xa = to_f32(a[k].t[j]), xb = to_f32(a[k].t[j + 1]);
-            a[k].t[j] = from_f32<T>(xa * w.x - xb * w.y);
-            a[k].t[j + 1] = from_f32<T>(xa * w.y + xb * w.x);
+            const Pair w = ct[(step[k] * V + j) / 2];
+            const Real xa = to_f32(a[k].t[j]), xb = to_f32(a[k].t[j + 1]);
+            a[k].t[j] = from_f32<T>(static_cast<float>(xa * w.x - xb * w.y));
+            a[k].t[j + 1] = from_f32<T>(static_cast<float>(xa * w.y + xb * w.x));
           }
         }
       }
