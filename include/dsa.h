@@ -354,8 +354,10 @@ dsa_status dsa_rope_query(void* q, const int32_t* pos, int32_t n_q, float theta,
  *   beta_fast >= beta_slow > 0; NTK: rot_dim > 2.  factor, original_len and the betas are ignored where unused.
  *
  * dsa_rope: dims [offset, offset + rot_dim) of every head of x [n_tokens, n_heads, dim] turned to pos[token]
- * (int32 [n_tokens] on the device, of either sign), each value rounded once to dtype (bf16, f16 or f32):
+ * (int32 [n_tokens] on the device, of either sign), in dtype (bf16, f16 or f32):
  *   out[a] = mscale (x[a] cos - x[b] sin),  out[b] = mscale (x[a] sin + x[b] cos)  for each pair (a, b).
+ * f32 values are formed in double and rounded once; bf16 and f16 values are formed in fp32, to within
+ * 3 * 2^-24 mscale (|x[a]| + |x[b]|), and then rounded.
  * out == x with equal strides works in place and touches the rotated dims only; otherwise out must not overlap x
  * and receives the other dims unchanged.  backward != 0 applies the transposed map (the angle negated, mscale
  * kept): the gradient of x from the gradient of out.

@@ -122,18 +122,19 @@ union Pack {
 };
 
 // One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared memory; then
-// each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (16-bit types: 2;
-// 4 take 97 registers, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes: 8,192 tokens x 64
-// heads x 64 dims in bf16 25.8 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.
+// each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (4 take 97
+// registers in bf16, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes: 8,192 tokens x 64
+// heads x 64 dims in bf16 25.7 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.  fp32 is held to 4 blocks per SM:
+// 4,097 tokens x 8 heads of 128 dims, 64 turned, 8.3 us (11.1 at 72 registers and 3 blocks; 8.0 with fp32 arithmetic).
 template <typename T>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 0 : 4) rope_kernel(const __grid_constant__ Params p,
                                                        const __grid_constant__ Freqs fr) {
   grid_dependency_sync();
   using Real = typename Turn<T>::Real;
   using Pair = typename Turn<T>::Pair;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   Pair* cs = reinterpret_cast<Pair*>(rope_smem);  // [tok_per_cta][rot / 2]
-  constexpr int V = Vec<T>::N, UNROLL = sizeof(T) == 2 ? 2 : 4;
+  constexpr int V = Vec<T>::N, UNROLL = 2;
   const int32_t tg = static_cast<int32_t>(quotient(blockIdx.x, p.by_groups));
   const int32_t t0 = tg * p.tok_per_cta;
   const int32_t h0 = (static_cast<int32_t>(blockIdx.x) - tg * p.head_groups) * p.head_per_cta;
