@@ -382,7 +382,7 @@ def _sparse_mla_attn4(q, kv, idx, k, softmax_scale, rows, out, lse, workspace):
         _refuse("lse must be a contiguous fp32 tensor [n_q, 64]")
     if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         _refuse("workspace must be a contiguous uint8 tensor")
-    stream = _on_device(q, idx, out, lse, workspace, *_held(kv)[:1])
+    stream = _on_device(q, idx, out, lse, workspace, *_held(kv))
     lib = load()
     if workspace is None:
         need = lib.dsa_sparse_mla_workspace_bytes(n, k, kv)
@@ -485,7 +485,7 @@ def latent_append(x, pos, cache: CacheView, gamma=None, eps: float = 1e-6, rope=
     if gamma is not None and (gamma.dtype is not torch.float32 or gamma.dim() != 1 or gamma.numel() != 512
                               or not gamma.is_contiguous()):
         _refuse("gamma must be a contiguous fp32 tensor of 512 entries")
-    stream = _on_device(x, pos, seq, gamma, *_held(cache)[:1])
+    stream = _on_device(x, pos, seq, gamma, *_held(cache))
     _check(load().dsa_latent_append(x.data_ptr(), dt, xs[0] if n > 1 else 576, n, _ptr(gamma), eps, rope, _ptr(seq),
                                     pos.data_ptr(), cache, stream))
     return cache
@@ -504,7 +504,7 @@ def latent_read(cache: CacheView, pos, seq=None, out=None):
         out = torch.empty(n, 576, dtype=torch.bfloat16, device=pos.device)
     elif out.dtype is not torch.bfloat16 or out.shape != (n, 576) or out.stride(1) != 1:
         _refuse("out must be a bf16 tensor [n, 576] with contiguous rows")
-    stream = _on_device(pos, seq, out, *_held(cache)[:1])
+    stream = _on_device(pos, seq, out, *_held(cache))
     _check(load().dsa_latent_read(cache, _ptr(seq), pos.data_ptr(), n, out.data_ptr(), out.stride(0) if n > 1 else 576,
                                   stream))
     return out

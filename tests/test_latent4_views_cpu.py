@@ -1,4 +1,5 @@
-"""Cache views as the entry points of the 4-bit latent cache take them: built field by field."""
+"""Cache views as the entry points of the 4-bit latent cache take them: built field by field, and with a tensor on a
+device of its own."""
 import pytest
 import torch
 
@@ -42,3 +43,18 @@ def test_views_without_tensors_of_their_own(lib, which):
     view = B.CacheView.from_buffer_copy(list(views())[which])
     for call in calls(view):
         assert "CUDA device" in refused(call)
+
+
+class Elsewhere:
+    device = "cuda:1"
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("which,part", [(0, 2), (0, 3), (1, 1), (1, 2), (1, 3)])
+def test_every_tensor_of_a_view_lies_on_the_calls_device(lib, which, part):
+    view = list(views())[which]
+    view._keep = tuple(Elsewhere() if i == part else t for i, t in enumerate(view._keep))
+    for call in calls(view):
+        assert "cuda:1" in refused(call)
