@@ -5,10 +5,12 @@
 //   * a cache value c * 2^e (e2m1 times a power of two in [2^-13, 2^13]) is an e5m2 number, exactly.  Four of them
 //     decode with one byte permutation (a table of the block's eight magnitudes) and one logical operation;
 //   * q is scaled per head by a power of two to a largest magnitude in [128, 256) and split into the nearest e4m3
-//     number and 16 times the rest, also e4m3: 8 significant bits, all that bf16 has.  The two parts are 128 rows of
-//     one product, summed with the factor 1/16 in the softmax;
-//   * p is split into the nearest e4m3 number and the nearest e5m2 number of the rest (7 to 8 bits, as bf16, and a
-//     floor of 2^-20 of the row's largest probability), two products into the same accumulator.
+//     number and 16 times the rest, also e4m3: 8 significant bits, all that bf16 has, down to 2^-13 of the head's largest
+//     value (smaller ones are off by up to 2^-21 of it).  The two parts are 128 rows of one product, summed with the
+//     factor 1/16 in the softmax;
+//   * p is rounded to f16 and split into the nearest e4m3 number and the nearest e5m2 number of the rest: off by less than
+//     2^-8 of it, the most that bf16 is, and by up to 2^-18 of the row's largest probability where p is below 2^-10 of that.
+//     Two products into the same accumulator; the sum of p is of the unsplit fp32 values.
 //   S[q part, key]  = Q[part, 0:576] . KV[key, 0:576]    M = 128, N = 128, K = 32: 18 steps of 64 clocks
 //   O^T[dim, head] += V^T[dim, key] . P[head, key]       M = 128 dims x 4, N = 64, K = 32, 2 parts: 32 steps of 48 clocks
 // so a tile of 128 keys takes the tensor core about 2,700 clocks, the second product at the rate of shared memory (6 KB per
@@ -68,7 +70,9 @@ constexpr int B_SFULL = 0, B_RFREE = 1, B_SREAD = 2, B_PFULL = 3, B_PVDONE = 4, 
               B_EMPTY = B_FULL + SLOTS;
 
 // p is 2^(z - m + 4), held as e = p / 256 = 2^(z + nn), nn = BIAS - m: p is at most 2^8 (e4m3 ends at 448) while the running
-// maximum m trails the true one by up to GROW, and with e5m2's smallest step of 2^-16 exact to 2^-20 of the largest.
+// maximum m trails the true one by up to GROW.  Below p = 2^-6 the e4m3 part is subnormal and the rest up to 2^-10, whose e5m2
+// number is off by up to 2^-14: 2^-18 of a largest p of 2^4 or more.  A smaller GROW would keep more of small p and move the
+// maximum more often: 2 gives 2^-20, and 512 rows 193 us for 175; 3 gives 2^-19 and 181.
 constexpr float BIAS = -4.f, GROW = 4.f;
 static_assert(BIAS + GROW == 0.f, "e <= 1");
 
@@ -133,7 +137,7 @@ __device__ __forceinline__ void split_q(const uint4& raw, float mul, uint2& hi, 
   const __half2 sixteen = __float2half2_rn(16.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // exact in f16: 8 significant bits, at most 256 (what lies below f16's range is below 2^-31 of the head's largest)
+    // exact in f16: 8 significant bits, at most 256 (f16's smallest step is 2^-31 of the head's largest)
     const __half2 v = __floats2half2_rn(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
     const __half2_raw vr = v;
     h[i] = __nv_cvt_halfraw2_to_fp8x2(vr, __NV_SATFINITE, __NV_E4M3);
