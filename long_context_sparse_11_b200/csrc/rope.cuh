@@ -121,13 +121,16 @@ union Pack {
   T t[Vec<T>::N];
 };
 
+template <typename T>
+constexpr int MIN_BLOCKS = sizeof(T) == 2 ? 0 : 4;  // per SM; 0: as many as the registers leave
+
 // One CTA: tok_per_cta tokens x head_per_cta heads.  The tokens' sines and cosines are formed once, in shared memory; then
 // each thread takes 16-byte steps (half layout: one in each half), UNROLL at a time with their loads first (4 take 97
 // registers in bf16, and a prefill chunk's queries 41 instead of 26 us).  Bound by the tensor's bytes: 8,192 tokens x 64
 // heads x 64 dims in bf16 25.7 us, 5.2 TB/s; a decode step's 32 tokens 4 us alone, a launch.  fp32 is held to 4 blocks per SM:
 // 4,097 tokens x 8 heads of 128 dims, 64 turned, 8.3 us (11.1 at 72 registers and 3 blocks; 8.0 with fp32 arithmetic).
 template <typename T>
-__global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 0 : 4) rope_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS<T>) rope_kernel(const __grid_constant__ Params p,
                                                        const __grid_constant__ Freqs fr) {
   grid_dependency_sync();
   using Real = typename Turn<T>::Real;
