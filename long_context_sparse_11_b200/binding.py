@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdsa.so")
 
 DSA_BF16, DSA_E4M3, DSA_MXFP4, DSA_F16, DSA_F32 = 0, 1, 2, 3, 4
-MXFP4_ROW = 320  # bytes of a 4-bit latent row
+MXFP4_ROW = 320  # bytes of a 4-bit latent row, a format of this library (not OCP MX)
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "stale index handle", 4: "device wait timed out",
           5: "CUDA error", 6: "workspace too small", 7: "index or page out of range",
           8: "input value outside the supported range"}
@@ -39,6 +39,7 @@ class CacheView(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("scale", c_void_p), ("block_table", c_void_p), ("seq_lens", c_void_p),
                 ("row_stride", c_int64), ("n_tokens", c_int64), ("dim", c_int32), ("dtype", c_int32),
                 ("max_pages", c_int32), ("batch", c_int32)]
+    _places = ()  # tensors whose devices a call compares with its own: none for a view filled in field by field
 
 
 class IndexHandle(ctypes.Structure):
@@ -183,9 +184,9 @@ def _on_device(*tensors) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _held(view) -> tuple:
-    """The tensors that a view of :func:`paged_view` holds; none for one filled in field by field."""
-    return getattr(view, "_keep", ())
+def _places(tensors) -> tuple:
+    """The first of a view's tensors, or all where they lie on several devices (looked at once, when the view is made)."""
+    return tensors[:1] if all(t.device == tensors[0].device for t in tensors) else tensors
 
 
 def _i32(t, n: int, name: str):
@@ -215,6 +216,8 @@ def paged_view(pool, scale, block_table, seq_lens, rows_per_seq: int = 1) -> Cac
     cache in 4 bits, pool [n_pages,64,320] uint8 (:func:`latent_pool4`), for the attention of
     :func:`sparse_mla_attn` and :class:`IndexShareGroup`, :func:`latent_append` and :func:`latent_read`.
 
+    A prompt's query rows over one sequence: that sequence's block-table row and a length once per query row.
+
     rows_per_seq > 1 presents each sequence as that many consecutive entries sharing its pages
     and length (the block-table rows and lengths are repeated once, here; the pages are not
     copied): the view through which every MTP verification row is scored, selected and attended
@@ -229,11 +232,12 @@ def paged_view(pool, scale, block_table, seq_lens, rows_per_seq: int = 1) -> Cac
     if scale is None:
         v = CacheView(pool.data_ptr(), None, block_table.data_ptr(), seq_lens.data_ptr(), MXFP4_ROW, n_pages * 64, 576,
                       DSA_MXFP4, block_table.shape[1], block_table.shape[0])
-        v._keep = (pool, scale, block_table, seq_lens)
+        v._keep, v._places = (pool, scale, block_table, seq_lens), (pool,)
         return v
     v = CacheView(pool.data_ptr(), scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), dim,
                   n_pages * 64, dim, DSA_E4M3, block_table.shape[1], block_table.shape[0])
     v._keep = (pool, scale, block_table, seq_lens)
+    v._places = _places(v._keep)
     return v
 
 
@@ -382,7 +386,7 @@ def _sparse_mla_attn4(q, kv, idx, k, softmax_scale, rows, out, lse, workspace):
         _refuse("lse must be a contiguous fp32 tensor [n_q, 64]")
     if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         _refuse("workspace must be a contiguous uint8 tensor")
-    stream = _on_device(q, idx, out, lse, workspace, *_held(kv))
+    stream = _on_device(q, idx, out, lse, workspace, *kv._places)
     lib = load()
     if workspace is None:
         need = lib.dsa_sparse_mla_workspace_bytes(n, k, kv)
@@ -485,7 +489,7 @@ def latent_append(x, pos, cache: CacheView, gamma=None, eps: float = 1e-6, rope=
     if gamma is not None and (gamma.dtype is not torch.float32 or gamma.dim() != 1 or gamma.numel() != 512
                               or not gamma.is_contiguous()):
         _refuse("gamma must be a contiguous fp32 tensor of 512 entries")
-    stream = _on_device(x, pos, seq, gamma, *_held(cache))
+    stream = _on_device(x, pos, seq, gamma, *cache._places)
     _check(load().dsa_latent_append(x.data_ptr(), dt, xs[0] if n > 1 else 576, n, _ptr(gamma), eps, rope, _ptr(seq),
                                     pos.data_ptr(), cache, stream))
     return cache
@@ -504,7 +508,7 @@ def latent_read(cache: CacheView, pos, seq=None, out=None):
         out = torch.empty(n, 576, dtype=torch.bfloat16, device=pos.device)
     elif out.dtype is not torch.bfloat16 or out.shape != (n, 576) or out.stride(1) != 1:
         _refuse("out must be a bf16 tensor [n, 576] with contiguous rows")
-    stream = _on_device(pos, seq, out, *_held(cache))
+    stream = _on_device(pos, seq, out, *cache._places)
     _check(load().dsa_latent_read(cache, _ptr(seq), pos.data_ptr(), n, out.data_ptr(), out.stride(0) if n > 1 else 576,
                                   stream))
     return out

@@ -45,16 +45,26 @@ def test_views_without_tensors_of_their_own(lib, which):
         assert "CUDA device" in refused(call)
 
 
-class Elsewhere:
-    device = "cuda:1"
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lies on another GPU."""
+
+    device = torch.device("cuda:1")
 
     def get_device(self):
         return 1
 
 
-@pytest.mark.parametrize("which,part", [(0, 2), (0, 3), (1, 1), (1, 2), (1, 3)])
-def test_every_tensor_of_a_view_lies_on_the_calls_device(lib, which, part):
-    view = list(views())[which]
-    view._keep = tuple(Elsewhere() if i == part else t for i, t in enumerate(view._keep))
-    for call in calls(view):
-        assert "cuda:1" in refused(call)
+@pytest.mark.parametrize("part", [1, 2, 3])
+def test_every_tensor_of_an_e4m3_view_lies_on_the_calls_device(lib, part):
+    made = [torch.zeros(4, 64, 576, dtype=torch.uint8), torch.zeros(4, 64), torch.zeros(2, 2, dtype=torch.int32),
+            torch.ones(2, dtype=torch.int32)]
+    made[part] = made[part].as_subclass(Elsewhere)
+    for call in calls(dsa.paged_view(*made)):
+        assert "tensors on cpu and cuda:1" in refused(call)
+
+
+@pytest.mark.parametrize("part", [2, 3])
+def test_every_tensor_of_a_4bit_view_lies_on_one_device(lib, part):
+    made = [dsa.latent_pool4(4, "cpu"), None, torch.zeros(2, 2, dtype=torch.int32), torch.ones(2, dtype=torch.int32)]
+    made[part] = made[part].as_subclass(Elsewhere)
+    assert "cuda:1" in refused(lambda: dsa.paged_view(*made))
