@@ -87,6 +87,8 @@ typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_MXFP4 = 2, DSA_F16 = 3, DSA_F32 =
  *          magnitude code of value i, bit 8i + 7 is the sign of value i for i < 4, bit 8i + 3 the sign
  *          of value 4 + i.  Bytes 288..305: e + 127 of blocks 0..17; 141 with 32 codes 7: every value of
  *          the block is NaN; other bytes outside 114..140 have no meaning.  Bytes 306..319 are zero.
+ *          This is not the OCP MX format of a similar name: its exponents end at +-13 (magnitudes above 49,152
+ *          saturate, those up to 2^-15 become 0), follow another rule, and its bits are in another order.
  */
 typedef struct {
   const void* data;
@@ -206,7 +208,9 @@ dsa_status dsa_topk(const float* scores, int64_t ld, int32_t n_rows, const int32
  *        (MTP rows sharing row 0's selection).  -1 entries are skipped.
  *   kv   dim 576.  Dense bf16: idx values are token rows of kv.  Paged e4m3: idx row i is
  *        sequence i and its values are token positions s < seq_lens[i].  Paged MXFP4: the same;
- *        q may hold any finite bf16 value, and a head whose q is not finite gets NaN.
+ *        q may hold any finite bf16 value (values below 2^-13 of their head's largest are held to 2^-21 of
+ *        that), and a head whose q is not finite gets NaN.  There a probability is held to 2^-8 of itself or
+ *        2^-18 of the row's largest, whichever is more, before its product with the row.
  *   A row with no valid index gets out = 0 and lse = -inf.
  *   Paged e4m3 caches: the products run on f16 operands (e4m3 values are exact in f16), so q is
  *   converted from bf16 to f16 and must lie within the f16 range, |q| < 65520; a larger value
@@ -383,8 +387,8 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, const void* x, void* out, int32_t
 /* ---------------------------------------------------------------------------------------
  * New latent rows into a paged cache, normalised, rotated and quantised on the way in one launch:
  *   y[r] = [ x[r, :512] / sqrt(mean(x[r, :512]^2) + eps) * gamma  ||  rope(x[r, 512:], pos[r]) ]
- * (gamma NULL: the first 512 dims as they are; rope NULL: the last 64 as they are), formed in double, rounded to
- * fp32, and stored at position pos[r] of sequence seq[r] (r itself when seq is NULL) of `cache`:
+ * (gamma NULL: the first 512 dims as they are; rope NULL: the last 64 as they are), formed to at least 48 bits (the
+ * mean and the rotation in double, the products with gamma in pairs of fp32), rounded to fp32, and stored at position pos[r] of sequence seq[r] (r itself when seq is NULL) of `cache`:
  *   e4m3    the rule of dsa_cache_write_e4m3 (one scale per row);
  *   MXFP4   per block of 32: e = the least exponent of [-13, 13] with amax <= 6 * 2^e, c = RNE(y / 2^e), magnitudes
  *           above 6 * 2^13 saturating; a block with a NaN reads back as NaN.

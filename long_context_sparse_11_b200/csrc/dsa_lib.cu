@@ -466,11 +466,12 @@ bool mla_query_prepass(int32_t n_q, int32_t k, int sms) {
 }
 
 // The 4-bit attention's schedule, one CTA per SM: the same number of whole rows for each, and the rows that remain (fewer than
-// SMs) in as many equal parts as there are SMs for, one to a CTA.  (Equal contiguous ranges of all tiles cut more rows, and a
-// cut costs a CTA another query and output and the call its merge, together about as much as 8 tiles: at k = 2,048, with the
-// merge, 31 rows 30.8 us in ranges and 26.7 in parts, 160 rows 73.2 and 68.1, 220 rows 97.0 and 86.6, 512 rows 193.5 and
-// 185.7, 1,024 rows 370 and 349.)  Parts that shorten a row by fewer than 3 tiles are not worth the merge: 330 rows of 256 keys
-// 37.9 us in parts of one tile, 34.9 whole.
+// SMs) in as many equal parts as there are SMs for, one to a CTA.  Times here: k = 2,048, every row over 8,192 tokens of its
+// own, with the merge.  Equal contiguous ranges of all tiles cut more rows, and a cut costs a CTA another query and output:
+// 160 rows 81.1 us in ranges and 75.7 in parts, 220 rows 107.6 and 98.6, 512 rows 224 and 217, 1,024 rows 412 and 416.  The
+// parts come in steps: 49 rows (3 parts) 31.4 us, 50 (2) 35.4, 74 (2) 38.9, 75 (whole, on 75 SMs) 52.9, 148 61.8.
+// Parts that shorten a row by fewer than 3 tiles are not made: 330 rows of 256 keys take 41.3 us in parts of one tile and
+// whole, and whole rows need neither the second launch nor a workspace.
 struct Plan4 {
   int32_t tiles_per_row = 0, grid = 0, whole_rows = 0, cut_rows = 0, parts = 1;
   int64_t tiles = 0;

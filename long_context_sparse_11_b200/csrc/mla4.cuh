@@ -14,8 +14,8 @@
 //   S[q part, key]  = Q[part, 0:576] . KV[key, 0:576]    M = 128, N = 128, K = 32: 18 steps of 64 clocks
 //   O^T[dim, head] += V^T[dim, key] . P[head, key]       M = 128 dims x 4, N = 64, K = 32, 2 parts: 32 steps of 48 clocks
 // so a tile of 128 keys takes the tensor core about 2,700 clocks, the second product at the rate of shared memory (6 KB per
-// step).  A tile in fact takes about 4,000 (32 x 5 rows of 2,048 keys 67 us with the merge; 512 rows 177 us, 824 TFLOP/s of
-// the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the products read, and the
+// step).  A tile in fact takes about 4,000 (with the merge, 32 x 5 rows of 2,048 keys 66 us; 512 rows of one sequence 173 to 175
+// us, 840 TFLOP/s of the products as they are defined): its 72 KB of decoded values, written beside the 272 KB that the products read, and the
 // instructions of decode and softmax share the SM with it (512 rows: issue slots 56% busy, the L1 data pipe 59%).
 //
 // The chain of one tile (rows, decode, S, softmax, PV) is several times that long, so three tiles are in flight: a decoded tile
